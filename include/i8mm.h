@@ -518,6 +518,149 @@ void i8mm_test_fail_product_launches(int count);
 i8mm_status i8mm_calib_mfma_i8(const int8_t* codes, int64_t blocks, int64_t iters, int32_t* out,
                                hipStream_t stream);
 
+/*
+ * Around a frozen int8 layer that is being adapted: layer norm, low-rank
+ * adapters and gradient clipping.
+ *
+ * The conventions above hold except for these:
+ *   - Matrices have a row stride argument (ld..., in elements, at least the
+ *     row length); their columns are adjacent.
+ *   - A tensor's element type is passed as an i8mm_dtype value; parameters' gradients and
+ *     row statistics are fp32. Sums and statistics are held in fp32 or
+ *     more, and each 16-bit result is rounded once, to nearest even.
+ *   - s = 0 is accepted: no row is read or written, and sums over rows are 0;
+ *     pointers to what has no rows may then be NULL.
+ *   - Outputs must not overlap inputs, unless an entry point says so.
+ *   - Results do not change from call to call: no sum's order does.
+ */
+typedef enum { I8MM_F16 = 0, I8MM_BF16 = 1, I8MM_F32 = 2 } i8mm_dtype;
+
+/* Longest row of the layer norms. */
+#define I8MM_NORM_MAX_H 1048576
+
+/*
+ * Layer norm of each row: with mean_i = sum_j x_ij / h, var_i =
+ * sum_j (x_ij - mean_i)^2 / h and rstd_i = 1 / sqrt(var_i + eps),
+ *   Y_ij = (x_ij - mean_i) rstd_i weight_j + bias_j.
+ *
+ * X: [s, h] of x_type (read), row stride ldx. weight, bias: [h] of w_type,
+ * which is x_type or I8MM_F32; bias may be NULL. Y: [s, h] of x_type
+ * (written), row stride ldy; Y may be X itself. mean, rstd: [s] fp32
+ * (written), or NULL. eps: finite, >= 0. s: 0 .. 2^31 - 1; h: 1 ..
+ * I8MM_NORM_MAX_H, any value. Pointers need the alignment of their element.
+ * A NaN or infinity stays in its row.
+ */
+i8mm_status i8mm_layer_norm(const void* X, int64_t ldx, int32_t x_type, int64_t s, int64_t h,
+                            const void* weight, const void* bias, int32_t w_type, float eps,
+                            void* Y, int64_t ldy, float* mean, float* rstd, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_layer_norm_backward (0 for bad shapes). */
+size_t i8mm_layer_norm_backward_workspace_bytes(int64_t s, int64_t h);
+
+/*
+ * The gradients of i8mm_layer_norm for the gradient dY of Y: with
+ * n_ij = (x_ij - mean_i) rstd_i and g_ij = dY_ij weight_j,
+ *   dX_ij = rstd_i (g_ij - mean_j(g_ij) - n_ij mean_j(g_ij n_ij)),
+ *   d_weight_j = sum_i dY_ij n_ij,  d_bias_j = sum_i dY_ij.
+ *
+ * dY, X: [s, h] of x_type (read). weight: [h] of w_type; mean, rstd: [s], as
+ * written by i8mm_layer_norm for X. dX: [s, h] of x_type (written).
+ * d_weight, d_bias: [h] fp32 (written; all 0 if s = 0), each may be NULL.
+ * workspace: i8mm_layer_norm_backward_workspace_bytes(s, h) bytes, 256-byte
+ * aligned, contents unspecified before and after; NULL is accepted if
+ * d_weight and d_bias are NULL.
+ */
+i8mm_status i8mm_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int32_t x_type,
+                                     int64_t s, int64_t h, const void* weight, int32_t w_type,
+                                     const float* mean, const float* rstd, void* dX, int64_t lddx,
+                                     float* d_weight, float* d_bias, void* workspace, hipStream_t stream);
+
+/* Limits of the adapters: the rank, their number, and the tokens of a call. */
+#define I8MM_LORA_MAX_RANK 128
+#define I8MM_LORA_MAX_ADAPTERS 65535
+#define I8MM_LORA_MAX_ROWS 16777216
+
+/* Bytes of device workspace of i8mm_lora_forward (0 for bad shapes). */
+size_t i8mm_lora_forward_workspace_bytes(int64_t s, int64_t h, int64_t o, int64_t r);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection: row i of
+ * X carries the adapter g = ids[i], and
+ *   T_i = X_i A_g^T,  Y_i = base_i + scale_g T_i B_g.
+ * A row whose id is outside [0, n_adapters) has no adapter: T_i = 0 and
+ * Y_i = base_i. base is the projection's own output (i8mm_forward's C).
+ *
+ * X: [s, h] of `type` (I8MM_F16 or I8MM_BF16), row stride ldx. A:
+ * [n_adapters, r, h], B: [n_adapters, r, o] of `type`, dense; an adapter of a
+ * lower rank has zero rows. ids: [s] int32; scale: [n_adapters] fp32 (alpha /
+ * rank in the usual convention). base: [s, o] of `type`, row stride ldb, or
+ * NULL for zeros. Y: [s, o] of `type` (written), row stride ldy; Y may be
+ * base itself, with the same stride. T: [s, r] fp32 (written; what the
+ * backward pass reads), or NULL. The rows' order is free: rows of one
+ * adapter need not be adjacent, though adjacent ones cost less.
+ * h, o: multiples of 64, at least 64 and at most I8MM_MAX_H; r: 1 ..
+ * I8MM_LORA_MAX_RANK; n_adapters: 1 .. I8MM_LORA_MAX_ADAPTERS; s: 0 ..
+ * I8MM_LORA_MAX_ROWS. X, A, B, base and Y are 16-byte aligned, with strides
+ * that are multiples of 8. workspace:
+ * i8mm_lora_forward_workspace_bytes(s, h, o, r) bytes, 256-byte aligned,
+ * contents unspecified before and after.
+ * Values of another row, or of an adapter that a row does not carry, never
+ * reach it, NaN and infinity included.
+ */
+i8mm_status i8mm_lora_forward(const void* X, int64_t ldx, const void* A, const void* B, int32_t type,
+                              int64_t n_adapters, int64_t r, const int32_t* ids, const float* scale,
+                              const void* base, int64_t ldb, int64_t s, int64_t h, int64_t o,
+                              void* Y, int64_t ldy, float* T, void* workspace, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_lora_backward (0 for bad shapes). */
+size_t i8mm_lora_backward_workspace_bytes(int64_t s, int64_t h, int64_t o, int64_t r, int64_t n_adapters);
+
+/*
+ * The gradients of i8mm_lora_forward for the gradient dY of Y:
+ *   dT_i = scale_g dY_i B_g^T,  dX_i = base_i + dT_i A_g,
+ *   dA_g = sum over the rows of g of dT_i^T X_i,
+ *   dB_g = scale_g times the sum over the rows of g of T_i^T dY_i.
+ * base is the gradient that reaches X through the projection itself.
+ *
+ * dY: [s, o], X: [s, h] of `type`; T: [s, r] fp32, as written by
+ * i8mm_lora_forward; A, B, ids, scale as there. base: [s, h] of `type`, or
+ * NULL for zeros. dX: [s, h] of `type` (written), or NULL if it is not
+ * wanted; dX may be base itself, with the same stride. dA: [n_adapters, r, h],
+ * dB: [n_adapters, r, o] fp32 (written; 0 for an adapter that no row
+ * carries), 16-byte aligned. Limits and alignment as there. workspace:
+ * i8mm_lora_backward_workspace_bytes(...) bytes, 256-byte aligned, contents
+ * unspecified before and after.
+ */
+i8mm_status i8mm_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const float* T,
+                               const void* A, const void* B, int32_t type, int64_t n_adapters, int64_t r,
+                               const int32_t* ids, const float* scale, const void* base, int64_t ldb,
+                               int64_t s, int64_t h, int64_t o, void* dX, int64_t lddx, float* dA, float* dB,
+                               void* workspace, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_clip_grad_norm (0 for bad arguments). */
+size_t i8mm_clip_grad_norm_workspace_bytes(const int64_t* numels, int64_t n);
+
+/*
+ * The global gradient norm over n tensors, and clipping by it:
+ *   N = sqrt(sum of the squares of all elements of all tensors),
+ *   out = c g with c = min(1, max_norm / (N + 1e-6)).
+ * The squares are summed in fp64. A NaN in any gradient makes N, and with it
+ * every output, NaN; an infinite one makes c = 0.
+ *
+ * grads, outs: HOST arrays of n device pointers (outs may be NULL: the
+ * gradients are scaled in place; outs[i] may be grads[i]); numels: host
+ * array of n element counts (>= 0); types: host array of n i8mm_dtype
+ * values, each the type of grads[i] and outs[i]. The arrays are read before
+ * the call returns. Pointers need the alignment of their element; the
+ * pointer of an empty tensor may be NULL. max_norm: >= 0, +inf for the norm
+ * alone. total_norm: [1] fp32 (written): N. workspace:
+ * i8mm_clip_grad_norm_workspace_bytes(numels, n) bytes, 256-byte aligned,
+ * contents unspecified before and after. n = 0 gives N = 0.
+ */
+i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                                const int32_t* types, int64_t n, float max_norm, void* workspace,
+                                float* total_norm, hipStream_t stream);
+
 /* Library version string (static storage). */
 const char* i8mm_version(void);
 

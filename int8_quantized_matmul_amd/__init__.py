@@ -14,7 +14,7 @@ at Scale" (paper-graph-ui digest), "The Full LLM.int8() Algorithm".
 from __future__ import annotations
 
 import ctypes
-from typing import Dict, Optional, Tuple
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
@@ -45,6 +45,12 @@ __all__ = [
     "SCHEMES",
     "quantize_weights",
     "variant_forward",
+    "layer_norm",
+    "layer_norm_backward",
+    "lora_forward",
+    "lora_backward",
+    "LORA_MAX_RANK",
+    "clip_grad_norm",
     "forward_workspace",
     "forward_workspace_views",
     "x_o_stride",
@@ -72,6 +78,8 @@ ACC_BYTES = _native.header_define("I8MM_FORWARD_ACC_BYTES")
 NOALLOC_SCRATCH_BYTES = _native.header_define("I8MM_NOALLOC_SCRATCH_BYTES")
 # Fewest rows forward_inline_quant takes (I8MM_INLINE_QUANT_MIN_ROWS).
 INLINE_QUANT_MIN_ROWS = _native.header_define("I8MM_INLINE_QUANT_MIN_ROWS")
+# Largest rank of the adapters (I8MM_LORA_MAX_RANK).
+LORA_MAX_RANK = _native.header_define("I8MM_LORA_MAX_RANK")
 
 
 class I8MMError(RuntimeError):
@@ -588,3 +596,253 @@ def calib_mfma_i8(codes: torch.Tensor, iters: int, out: torch.Tensor) -> int:
                                  _dev(out, "out", torch.int32, (blocks * 256,)), _stream(codes))
     _check(st, "calib_mfma_i8")
     return blocks * 4 * 32 * iters * 65536
+
+
+# ---------------------------------------------------------------- around an adapted layer
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # i8mm_dtype
+
+
+def _row_stride(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
+    """The row stride of a GPU matrix whose columns are adjacent; what the
+    C ABI cannot see is checked here."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on cuda:{device} "
+                         f"(got {t.dtype} of shape {tuple(t.shape)} on {t.device})")
+    ld, step = t.stride()
+    if shape[0] <= 1:                   # the stride of a single row says nothing, no row has no strides
+        ld, step = shape[1], step if shape[0] else 1
+    if (step != 1 and shape[1] > 1) or ld < shape[1]:
+        raise ValueError(f"{name} must have adjacent columns and rows that do not overlap (strides {t.stride()})")
+    return ld
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
+    """The pointer of a contiguous GPU tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on cuda:{device} "
+                         f"(got {t.dtype} of shape {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
+
+
+def _gpu_of(t: torch.Tensor, name: str, types) -> int:
+    """The index of the GPU that t is on, which has to be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be one of {types} (got {t.dtype})")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.get_device()
+
+
+def _matrix_of(t: torch.Tensor, name: str, types) -> int:
+    dev = _gpu_of(t, name, types)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix (got shape {tuple(t.shape)})")
+    return dev
+
+
+def _scratch(nbytes: int, what: str, workspace: Optional[torch.Tensor], device: torch.device) -> torch.Tensor:
+    """The caller's workspace, checked, or a new one."""
+    if nbytes == 0:
+        raise I8MMError(f"{what}: invalid shape")
+    if workspace is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.numel() < nbytes or not workspace.is_contiguous() \
+            or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {device}")
+    return workspace
+
+
+_NORM_TYPES = (torch.float16, torch.bfloat16, torch.float32)
+
+
+def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               Y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+               rstd: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm of the rows of X [s, h] (fp16, bf16 or fp32; rows may be
+    strided): (Y = (X - mean) rstd weight + bias of X's type, mean fp32 [s],
+    rstd fp32 [s]). weight and bias [h] are of X's type or fp32. Y may be X."""
+    dev = _matrix_of(X, "X", _NORM_TYPES)
+    s, h = X.shape
+    if Y is None:
+        Y = torch.empty((s, h), dtype=X.dtype, device=X.device)
+    if mean is None:
+        mean = torch.empty((s,), dtype=torch.float32, device=X.device)
+    if rstd is None:
+        rstd = torch.empty((s,), dtype=torch.float32, device=X.device)
+    if weight.dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"weight must be {X.dtype} or torch.float32 (got {weight.dtype})")
+    st = _lib.i8mm_layer_norm(
+        X.data_ptr(), _row_stride(X, "X", X.dtype, X.shape, dev), _DTYPES[X.dtype], s, h,
+        _dense(weight, "weight", weight.dtype, (h,), dev),
+        None if bias is None else _dense(bias, "bias", weight.dtype, (h,), dev), _DTYPES[weight.dtype], eps,
+        Y.data_ptr(), _row_stride(Y, "Y", X.dtype, X.shape, dev), _dense(mean, "mean", torch.float32, (s,), dev),
+        _dense(rstd, "rstd", torch.float32, (s,), dev), _stream(X))
+    _check(st, "layer_norm")
+    return Y, mean, rstd
+
+
+def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor, param_grads: bool = True, dX: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None
+                        ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The gradients of layer_norm for dY, with its mean and rstd: (dX of X's
+    type, d_weight fp32 [h], d_bias fp32 [h]); the last two are None if
+    param_grads is false (a frozen norm). A workspace, if given, is a uint8
+    tensor of layer_norm_backward_workspace(s, h) bytes or more."""
+    dev = _matrix_of(X, "X", _NORM_TYPES)
+    s, h = X.shape
+    if dX is None:
+        dX = torch.empty((s, h), dtype=X.dtype, device=X.device)
+    if weight.dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"weight must be {X.dtype} or torch.float32 (got {weight.dtype})")
+    d_weight = d_bias = None
+    if param_grads:
+        d_weight, d_bias = torch.empty((2, h), dtype=torch.float32, device=X.device).unbind(0)
+        workspace = _scratch(layer_norm_backward_workspace(s, h), "layer_norm_backward", workspace, X.device)
+    st = _lib.i8mm_layer_norm_backward(
+        dY.data_ptr(), _row_stride(dY, "dY", X.dtype, X.shape, dev), X.data_ptr(),
+        _row_stride(X, "X", X.dtype, X.shape, dev), _DTYPES[X.dtype], s, h,
+        _dense(weight, "weight", weight.dtype, (h,), dev), _DTYPES[weight.dtype],
+        _dense(mean, "mean", torch.float32, (s,), dev), _dense(rstd, "rstd", torch.float32, (s,), dev),
+        dX.data_ptr(), _row_stride(dX, "dX", X.dtype, X.shape, dev),
+        *((d_weight.data_ptr(), d_bias.data_ptr(), workspace.data_ptr()) if param_grads else (None, None, None)),
+        _stream(X))
+    _check(st, "layer_norm_backward")
+    return dX, d_weight, d_bias
+
+
+def layer_norm_backward_workspace(s: int, h: int) -> int:
+    """Bytes of workspace that layer_norm_backward needs."""
+    return _lib.i8mm_layer_norm_backward_workspace_bytes(s, h)
+
+
+_LORA_TYPES = (torch.float16, torch.bfloat16)
+
+
+def _adapters(A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype, s: int,
+              h: int, o: int, dev: int):
+    """(G, r, and the pointers of the adapters, the ids and the factors)."""
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError(f"A and B must be [adapters, rank, features] (got {tuple(A.shape)}, {tuple(B.shape)})")
+    G, r = A.shape[0], A.shape[1]
+    return G, r, (_dense(A, "A", dtype, (G, r, h), dev), _dense(B, "B", dtype, (G, r, o), dev),
+                  _dense(ids, "ids", torch.int32, (s,), dev), _dense(scale, "scale", torch.float32, (G,), dev))
+
+
+def lora_forward_workspace(s: int, h: int, o: int, r: int) -> int:
+    """Bytes of workspace that lora_forward needs."""
+    return _lib.i8mm_lora_forward_workspace_bytes(s, h, o, r)
+
+
+def lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor,
+                 base: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                 T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Low-rank adapters beside a shared projection: row i of X [s, h] (fp16 or
+    bf16) carries adapter g = ids[i] (int32 [s]; none if outside [0, G)), and
+    Y_i = base_i + scale_g T_i B_g with T_i = X_i A_g^T. A [G, r, h] and
+    B [G, r, o] are of X's type, scale is fp32 [G]; base [s, o] is the
+    projection's output (None: zeros) and may be passed as Y too. Returns
+    (Y of X's type, T fp32 [s, r], which lora_backward reads)."""
+    dev = _matrix_of(X, "X", _LORA_TYPES)
+    s, h = X.shape
+    o = B.shape[-1]
+    G, r, (a, b, i, f) = _adapters(A, B, ids, scale, X.dtype, s, h, o, dev)
+    if Y is None:
+        Y = torch.empty((s, o), dtype=X.dtype, device=X.device)
+    if T is None:
+        T = torch.empty((s, r), dtype=torch.float32, device=X.device)
+    workspace = _scratch(lora_forward_workspace(s, h, o, r), "lora_forward", workspace, X.device)
+    st = _lib.i8mm_lora_forward(
+        X.data_ptr(), _row_stride(X, "X", X.dtype, X.shape, dev), a, b, _DTYPES[X.dtype], G, r, i, f,
+        *((None, 0) if base is None else (base.data_ptr(), _row_stride(base, "base", X.dtype, (s, o), dev))),
+        s, h, o, Y.data_ptr(), _row_stride(Y, "Y", X.dtype, (s, o), dev), _dense(T, "T", torch.float32, (s, r), dev),
+        workspace.data_ptr(), _stream(X))
+    _check(st, "lora_forward")
+    return Y, T
+
+
+def lora_backward_workspace(s: int, h: int, o: int, r: int, n_adapters: int) -> int:
+    """Bytes of workspace that lora_backward needs."""
+    return _lib.i8mm_lora_backward_workspace_bytes(s, h, o, r, n_adapters)
+
+
+def lora_backward(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                  ids: torch.Tensor, scale: torch.Tensor, base: Optional[torch.Tensor] = None,
+                  input_grad: bool = True, dX: Optional[torch.Tensor] = None, dA: Optional[torch.Tensor] = None,
+                  dB: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                  ) -> Tuple[Optional[torch.Tensor], torch.Tensor, torch.Tensor]:
+    """The gradients of lora_forward for dY [s, o], with its T: (dX [s, h] of
+    X's type, dA fp32 [G, r, h], dB fp32 [G, r, o]; zero for an adapter that
+    no row carries). base [s, h] is the gradient that reaches X through the
+    projection itself (None: zeros) and may be passed as dX too; dX is None
+    if input_grad is false."""
+    dev = _matrix_of(X, "X", _LORA_TYPES)
+    s, h = X.shape
+    o = B.shape[-1]
+    G, r, (a, b, i, f) = _adapters(A, B, ids, scale, X.dtype, s, h, o, dev)
+    if not input_grad:
+        dX = base = None
+    elif dX is None:
+        dX = torch.empty((s, h), dtype=X.dtype, device=X.device)
+    if dA is None:
+        dA = torch.empty((G, r, h), dtype=torch.float32, device=X.device)
+    if dB is None:
+        dB = torch.empty((G, r, o), dtype=torch.float32, device=X.device)
+    workspace = _scratch(lora_backward_workspace(s, h, o, r, G), "lora_backward", workspace, X.device)
+    st = _lib.i8mm_lora_backward(
+        dY.data_ptr(), _row_stride(dY, "dY", X.dtype, (s, o), dev), X.data_ptr(),
+        _row_stride(X, "X", X.dtype, X.shape, dev), _dense(T, "T", torch.float32, (s, r), dev), a, b,
+        _DTYPES[X.dtype], G, r, i, f,
+        *((None, 0) if base is None else (base.data_ptr(), _row_stride(base, "base", X.dtype, (s, h), dev))),
+        s, h, o,
+        *((None, 0) if dX is None else (dX.data_ptr(), _row_stride(dX, "dX", X.dtype, (s, h), dev))),
+        _dense(dA, "dA", torch.float32, (G, r, h), dev), _dense(dB, "dB", torch.float32, (G, r, o), dev),
+        workspace.data_ptr(), _stream(X))
+    _check(st, "lora_backward")
+    return dX, dA, dB
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None, device: Optional[torch.device] = None) -> torch.Tensor:
+    """The global norm N over all gradients (contiguous GPU tensors, each fp16,
+    bf16 or fp32), as fp32 [1] on the GPU, and the gradients times
+    min(1, max_norm / (N + 1e-6)): in place, or into the tensors of `out`
+    (like grads, each of its gradient's type). device is only needed for an
+    empty list."""
+    grads = list(grads)
+    n = len(grads)
+    if n == 0:
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    else:
+        for g in grads:
+            _gpu_of(g, "grads", _NORM_TYPES)
+            if not g.is_contiguous():
+                raise ValueError("grads must be contiguous")
+        dev = grads[0].device
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError(f"out must hold {n} tensors (got {len(out)})")
+        for t, g in zip(out, grads):
+            _dense(t, "out", g.dtype, g.shape, dev.index)
+        outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    workspace = _scratch(_lib.i8mm_clip_grad_norm_workspace_bytes(numels, n), "clip_grad_norm", workspace, dev)
+    total = torch.empty((1,), dtype=torch.float32, device=dev)
+    st = _lib.i8mm_clip_grad_norm(
+        (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), outs, numels,
+        (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads]), n, max_norm, workspace.data_ptr(),
+        total.data_ptr(), _stream(total))
+    _check(st, "clip_grad_norm")
+    return total

@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(PKG, "lib", "libi8mm.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "i8mm.h")
 
 c_i64 = ctypes.c_int64
+c_i32 = ctypes.c_int32
 c_p = ctypes.c_void_p
 c_f = ctypes.c_float
 c_int = ctypes.c_int
@@ -45,6 +46,18 @@ _SIGNATURES = {
     "i8mm_forward_inline_quant": (c_int, [c_p, c_i64, c_i64, c_i64, c_f, c_p, c_p, c_p, c_p, c_p, c_p, c_p]),
     "i8mm_forward_noalloc": (c_int, [c_p, c_i64, c_i64, c_i64, c_f, c_p, c_p, c_p, c_p, c_p, c_p]),
     "i8mm_calib_mfma_i8": (c_int, [c_p, c_i64, c_i64, c_p, c_p]),
+    "i8mm_layer_norm": (c_int, [c_p, c_i64, c_i32, c_i64, c_i64, c_p, c_p, c_i32, c_f, c_p, c_i64, c_p, c_p, c_p]),
+    "i8mm_layer_norm_backward_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "i8mm_layer_norm_backward": (c_int, [c_p, c_i64, c_p, c_i64, c_i32, c_i64, c_i64, c_p, c_i32, c_p, c_p, c_p,
+                                         c_i64, c_p, c_p, c_p, c_p]),
+    "i8mm_lora_forward_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64]),
+    "i8mm_lora_forward": (c_int, [c_p, c_i64, c_p, c_p, c_i32, c_i64, c_i64, c_p, c_p, c_p, c_i64, c_i64, c_i64,
+                                  c_i64, c_p, c_i64, c_p, c_p, c_p]),
+    "i8mm_lora_backward_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64]),
+    "i8mm_lora_backward": (c_int, [c_p, c_i64, c_p, c_i64, c_p, c_p, c_p, c_i32, c_i64, c_i64, c_p, c_p, c_p, c_i64,
+                                   c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p]),
+    "i8mm_clip_grad_norm_workspace_bytes": (c_size, [c_p, c_i64]),
+    "i8mm_clip_grad_norm": (c_int, [c_p, c_p, c_p, c_p, c_i64, c_f, c_p, c_p, c_p]),
     "i8mm_test_fail_product_launches": (None, [c_int]),
     "i8mm_version": (ctypes.c_char_p, []),
     "i8mm_status_string": (ctypes.c_char_p, [c_int]),

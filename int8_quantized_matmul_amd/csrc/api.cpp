@@ -14,29 +14,15 @@
 #include <cstring>
 #include <mutex>
 
+#include "host_checks.h"
 #include "launch.h"
 
-namespace {
+namespace i8mm {
 
+namespace {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_ok[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-bool valid_shape_sh(int64_t s, int64_t h) {
-    return s >= 1 && h >= 64 && h % 64 == 0 && h <= I8MM_MAX_H && s <= (int64_t(1) << 31) - 1;
-}
-
-bool valid_o(int64_t o) { return o >= 64 && o % 64 == 0 && o <= (int64_t(1) << 31) - 64; }
-
-// The products address Wq (h o bytes) and W (2 h o bytes, fused product
-// only) through 32-bit buffer offsets.
-bool valid_w_extent(int64_t h, int64_t o) { return h * o < (int64_t(1) << 31); }
-
-// The dense fp16 product addresses Wp (2 h o bytes) with 32-bit offsets.
-bool valid_fp16_extent(int64_t h, int64_t o) { return 2 * h * o < (int64_t(1) << 31); }
+}  // namespace
 
 i8mm_status check_device() {
     int dev = -1;
@@ -59,7 +45,28 @@ i8mm_status check_device() {
     return ok ? I8MM_OK : I8MM_EDEVICE;
 }
 
-i8mm_status launched(hipError_t e) { return e == hipSuccess ? I8MM_OK : I8MM_ELAUNCH; }
+}  // namespace i8mm
+
+namespace {
+
+using i8mm::aligned16;
+using i8mm::check_device;
+using i8mm::kMaxDevices;
+using i8mm::launched;
+using i8mm::round_up;
+
+bool valid_shape_sh(int64_t s, int64_t h) {
+    return s >= 1 && h >= 64 && h % 64 == 0 && h <= I8MM_MAX_H && s <= (int64_t(1) << 31) - 1;
+}
+
+bool valid_o(int64_t o) { return o >= 64 && o % 64 == 0 && o <= (int64_t(1) << 31) - 64; }
+
+// The products address Wq (h o bytes) and W (2 h o bytes, fused product
+// only) through 32-bit buffer offsets.
+bool valid_w_extent(int64_t h, int64_t o) { return h * o < (int64_t(1) << 31); }
+
+// The dense fp16 product addresses Wp (2 h o bytes) with 32-bit offsets.
+bool valid_fp16_extent(int64_t h, int64_t o) { return 2 * h * o < (int64_t(1) << 31); }
 
 // Test hook: the number of one-call forwards whose product launch is to
 // report a failure without launching (i8mm_test_fail_product_launches).

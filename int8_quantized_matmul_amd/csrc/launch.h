@@ -128,4 +128,51 @@ hipError_t launch_outlier_matmul(const uint16_t* X_O, int64_t ldo,
 hipError_t launch_calib_mfma_i8(const int8_t* codes, int64_t blocks, int64_t iters, int32_t* out,
                                 hipStream_t stream);
 
+// Element types of the kernels around an adapted layer (the values of
+// i8mm_dtype).
+enum class Dtype { F16 = 0, BF16 = 1, F32 = 2 };
+
+// Layer norm of the rows of X and its gradients. Row strides in elements; wt
+// is xt or F32; b, mean and rstd may be null, as may dw and db. `part` holds
+// layer_norm_backward_parts(s) sums of 2 h floats (unused if dw and db are
+// null).
+hipError_t launch_layer_norm(const void* X, int64_t ldx, Dtype xt, int64_t s, int64_t h, const void* w, const void* b,
+                             Dtype wt, float eps, void* Y, int64_t ldy, float* mean, float* rstd, hipStream_t stream);
+int64_t layer_norm_backward_parts(int64_t s);
+hipError_t launch_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, Dtype xt, int64_t s,
+                                      int64_t h, const void* w, Dtype wt, const float* mean, const float* rstd,
+                                      void* dX, int64_t lddx, float* dw, float* db, float* part, hipStream_t stream);
+
+// What the adapter kernels share: the adapters A [G, r, h] and B [G, r, o]
+// of `type` (F16 or BF16), the adapter of each of the s tokens, and a factor
+// per adapter.
+struct LoraArgs {
+    const void* A;
+    const void* B;
+    Dtype type;
+    int64_t G;
+    int r;
+    const int32_t* ids;
+    const float* scale;
+    int64_t s, h, o;
+};
+
+// Y = base + scale (X A^T) B with T = X A^T in fp32; base and T may be null.
+size_t lora_forward_scratch(int64_t s, int64_t h, int64_t o, int64_t r);
+hipError_t launch_lora_forward(const LoraArgs& a, const void* X, int64_t ldx, const void* base, int64_t ldb, void* Y,
+                               int64_t ldy, float* T, void* workspace, hipStream_t stream);
+
+// The gradients of Y for dY, given T; base and dX may be null.
+size_t lora_backward_scratch(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G);
+hipError_t launch_lora_backward(const LoraArgs& a, const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                                const float* T, const void* base, int64_t ldb, void* dX, int64_t lddx, float* dA,
+                                float* dB, void* workspace, hipStream_t stream);
+
+// The norm over all n tensors to *total, and out = min(1, max_norm / norm)
+// in (in place if out is null). `workspace`: 256 bytes, then clip_parts()
+// doubles. The host arrays are read before the call returns.
+int64_t clip_parts(const int64_t* numel, int64_t n);
+hipError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* numel, const int32_t* types,
+                                 int64_t n, float max_norm, void* workspace, float* total, hipStream_t stream);
+
 }  // namespace i8mm
