@@ -599,24 +599,30 @@ def calib_mfma_i8(codes: torch.Tensor, iters: int, out: torch.Tensor) -> int:
 
 
 # ---------------------------------------------------------------- around an adapted layer
+#
+# These calls run in a few microseconds on the GPU while tokens are decoded,
+# so what they do on the host is kept short: one look at each tensor, none at
+# the outputs that they allocate themselves.
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # i8mm_dtype
+_LORA_TYPES = (torch.float16, torch.bfloat16)
 
 
-def _row_stride(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
-    """The row stride of a GPU matrix whose columns are adjacent; what the
-    C ABI cannot see is checked here."""
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> Tuple[int, int]:
+    """(pointer, row stride) of a GPU matrix whose columns are adjacent; what
+    the C ABI cannot see is checked here."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != device or t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on cuda:{device} "
                          f"(got {t.dtype} of shape {tuple(t.shape)} on {t.device})")
-    ld, step = t.stride()
     if shape[0] <= 1:                   # the stride of a single row says nothing, no row has no strides
-        ld, step = shape[1], step if shape[0] else 1
+        ld, step = shape[1], t.stride(1) if shape[0] else 1
+    else:
+        ld, step = t.stride()
     if (step != 1 and shape[1] > 1) or ld < shape[1]:
         raise ValueError(f"{name} must have adjacent columns and rows that do not overlap (strides {t.stride()})")
-    return ld
+    return t.data_ptr(), ld
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
@@ -633,20 +639,25 @@ def _gpu_of(t: torch.Tensor, name: str, types) -> int:
     """The index of the GPU that t is on, which has to be the current one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU, cuda:{torch.cuda.current_device()} (got {t.device})")
     if t.dtype not in types:
-        raise ValueError(f"{name} must be one of {types} (got {t.dtype})")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.get_device()
+        raise ValueError(f"{name} must be one of {tuple(types)} (got {t.dtype})")
+    return device
 
 
-def _matrix_of(t: torch.Tensor, name: str, types) -> int:
-    dev = _gpu_of(t, name, types)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix (got shape {tuple(t.shape)})")
-    return dev
+def _rows_of(X: torch.Tensor, types) -> Tuple[int, int, int, int, int]:
+    """(device, rows, columns, pointer, row stride) of the matrix X that a call goes by."""
+    device = _gpu_of(X, "X", types)
+    if X.dim() != 2:
+        raise ValueError(f"X must be a matrix (got shape {tuple(X.shape)})")
+    s, h = X.shape
+    return (device, s, h) + _matrix(X, "X", X.dtype, X.shape, device)
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _scratch(nbytes: int, what: str, workspace: Optional[torch.Tensor], device: torch.device) -> torch.Tensor:
@@ -654,14 +665,19 @@ def _scratch(nbytes: int, what: str, workspace: Optional[torch.Tensor], device: 
     if nbytes == 0:
         raise I8MMError(f"{what}: invalid shape")
     if workspace is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or workspace.numel() < nbytes or not workspace.is_contiguous() \
             or workspace.device != device:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {device}")
     return workspace
 
 
-_NORM_TYPES = (torch.float16, torch.bfloat16, torch.float32)
+def _norm_weight(weight: torch.Tensor, X: torch.Tensor, h: int, device: int) -> Tuple[int, int]:
+    """(pointer, i8mm_dtype) of a norm's weight, which is of X's type or fp32."""
+    wt = getattr(weight, "dtype", None)
+    if wt is not X.dtype and wt is not torch.float32:
+        raise ValueError(f"weight must be {X.dtype} or torch.float32 (got {wt})")
+    return _dense(weight, "weight", wt, (h,), device), _DTYPES[wt]
 
 
 def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
@@ -670,24 +686,32 @@ def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     """Layer norm of the rows of X [s, h] (fp16, bf16 or fp32; rows may be
     strided): (Y = (X - mean) rstd weight + bias of X's type, mean fp32 [s],
     rstd fp32 [s]). weight and bias [h] are of X's type or fp32. Y may be X."""
-    dev = _matrix_of(X, "X", _NORM_TYPES)
-    s, h = X.shape
+    dev, s, h, x, ldx = _rows_of(X, _DTYPES)
+    w, wt = _norm_weight(weight, X, h, dev)
+    b = None if bias is None else _dense(bias, "bias", weight.dtype, (h,), dev)
     if Y is None:
-        Y = torch.empty((s, h), dtype=X.dtype, device=X.device)
+        Y = X.new_empty((s, h))
+        y, ldy = Y.data_ptr(), h
+    else:
+        y, ldy = _matrix(Y, "Y", X.dtype, X.shape, dev)
     if mean is None:
-        mean = torch.empty((s,), dtype=torch.float32, device=X.device)
+        mean = X.new_empty(s, dtype=torch.float32)
+        m = mean.data_ptr()
+    else:
+        m = _dense(mean, "mean", torch.float32, (s,), dev)
     if rstd is None:
-        rstd = torch.empty((s,), dtype=torch.float32, device=X.device)
-    if weight.dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"weight must be {X.dtype} or torch.float32 (got {weight.dtype})")
-    st = _lib.i8mm_layer_norm(
-        X.data_ptr(), _row_stride(X, "X", X.dtype, X.shape, dev), _DTYPES[X.dtype], s, h,
-        _dense(weight, "weight", weight.dtype, (h,), dev),
-        None if bias is None else _dense(bias, "bias", weight.dtype, (h,), dev), _DTYPES[weight.dtype], eps,
-        Y.data_ptr(), _row_stride(Y, "Y", X.dtype, X.shape, dev), _dense(mean, "mean", torch.float32, (s,), dev),
-        _dense(rstd, "rstd", torch.float32, (s,), dev), _stream(X))
+        rstd = X.new_empty(s, dtype=torch.float32)
+        r = rstd.data_ptr()
+    else:
+        r = _dense(rstd, "rstd", torch.float32, (s,), dev)
+    st = _lib.i8mm_layer_norm(x, ldx, _DTYPES[X.dtype], s, h, w, b, wt, eps, y, ldy, m, r, _raw_stream(dev))
     _check(st, "layer_norm")
     return Y, mean, rstd
+
+
+def layer_norm_backward_workspace(s: int, h: int) -> int:
+    """Bytes of workspace that layer_norm_backward needs."""
+    return _lib.i8mm_layer_norm_backward_workspace_bytes(s, h)
 
 
 def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
@@ -698,44 +722,35 @@ def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor,
     type, d_weight fp32 [h], d_bias fp32 [h]); the last two are None if
     param_grads is false (a frozen norm). A workspace, if given, is a uint8
     tensor of layer_norm_backward_workspace(s, h) bytes or more."""
-    dev = _matrix_of(X, "X", _NORM_TYPES)
-    s, h = X.shape
+    dev, s, h, x, ldx = _rows_of(X, _DTYPES)
+    w, wt = _norm_weight(weight, X, h, dev)
+    dy, lddy = _matrix(dY, "dY", X.dtype, X.shape, dev)
+    m, r = _dense(mean, "mean", torch.float32, (s,), dev), _dense(rstd, "rstd", torch.float32, (s,), dev)
     if dX is None:
-        dX = torch.empty((s, h), dtype=X.dtype, device=X.device)
-    if weight.dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"weight must be {X.dtype} or torch.float32 (got {weight.dtype})")
-    d_weight = d_bias = None
+        dX = X.new_empty((s, h))
+        dx, lddx = dX.data_ptr(), h
+    else:
+        dx, lddx = _matrix(dX, "dX", X.dtype, X.shape, dev)
+    d_weight = d_bias = dw = db = ws = None
     if param_grads:
-        d_weight, d_bias = torch.empty((2, h), dtype=torch.float32, device=X.device).unbind(0)
+        d_weight, d_bias = X.new_empty(h, dtype=torch.float32), X.new_empty(h, dtype=torch.float32)
         workspace = _scratch(layer_norm_backward_workspace(s, h), "layer_norm_backward", workspace, X.device)
-    st = _lib.i8mm_layer_norm_backward(
-        dY.data_ptr(), _row_stride(dY, "dY", X.dtype, X.shape, dev), X.data_ptr(),
-        _row_stride(X, "X", X.dtype, X.shape, dev), _DTYPES[X.dtype], s, h,
-        _dense(weight, "weight", weight.dtype, (h,), dev), _DTYPES[weight.dtype],
-        _dense(mean, "mean", torch.float32, (s,), dev), _dense(rstd, "rstd", torch.float32, (s,), dev),
-        dX.data_ptr(), _row_stride(dX, "dX", X.dtype, X.shape, dev),
-        *((d_weight.data_ptr(), d_bias.data_ptr(), workspace.data_ptr()) if param_grads else (None, None, None)),
-        _stream(X))
+        dw, db, ws = d_weight.data_ptr(), d_bias.data_ptr(), workspace.data_ptr()
+    st = _lib.i8mm_layer_norm_backward(dy, lddy, x, ldx, _DTYPES[X.dtype], s, h, w, wt, m, r, dx, lddx, dw, db, ws,
+                                       _raw_stream(dev))
     _check(st, "layer_norm_backward")
     return dX, d_weight, d_bias
 
 
-def layer_norm_backward_workspace(s: int, h: int) -> int:
-    """Bytes of workspace that layer_norm_backward needs."""
-    return _lib.i8mm_layer_norm_backward_workspace_bytes(s, h)
-
-
-_LORA_TYPES = (torch.float16, torch.bfloat16)
-
-
-def _adapters(A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype, s: int,
-              h: int, o: int, dev: int):
-    """(G, r, and the pointers of the adapters, the ids and the factors)."""
+def _adapters(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor, s: int, h: int,
+              dev: int):
+    """(G, r, o, and the pointers of the adapters, the ids and the factors)."""
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError(f"A and B must be [adapters, rank, features] (got {tuple(A.shape)}, {tuple(B.shape)})")
-    G, r = A.shape[0], A.shape[1]
-    return G, r, (_dense(A, "A", dtype, (G, r, h), dev), _dense(B, "B", dtype, (G, r, o), dev),
-                  _dense(ids, "ids", torch.int32, (s,), dev), _dense(scale, "scale", torch.float32, (G,), dev))
+    G, r, _ = A.shape
+    o = B.shape[2]
+    return G, r, o, _dense(A, "A", X.dtype, (G, r, h), dev), _dense(B, "B", X.dtype, (G, r, o), dev), \
+        _dense(ids, "ids", torch.int32, (s,), dev), _dense(scale, "scale", torch.float32, (G,), dev)
 
 
 def lora_forward_workspace(s: int, h: int, o: int, r: int) -> int:
@@ -752,21 +767,25 @@ def lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.T
     Y_i = base_i + scale_g T_i B_g with T_i = X_i A_g^T. A [G, r, h] and
     B [G, r, o] are of X's type, scale is fp32 [G]; base [s, o] is the
     projection's output (None: zeros) and may be passed as Y too. Returns
-    (Y of X's type, T fp32 [s, r], which lora_backward reads)."""
-    dev = _matrix_of(X, "X", _LORA_TYPES)
-    s, h = X.shape
-    o = B.shape[-1]
-    G, r, (a, b, i, f) = _adapters(A, B, ids, scale, X.dtype, s, h, o, dev)
+    (Y of X's type, T fp32 [s, r], which lora_backward reads). A workspace, if
+    given, is a uint8 tensor of lora_forward_workspace(s, h, o, r) bytes or
+    more."""
+    dev, s, h, x, ldx = _rows_of(X, _LORA_TYPES)
+    G, r, o, a, b, i, f = _adapters(X, A, B, ids, scale, s, h, dev)
+    bp, ldb = (None, 0) if base is None else _matrix(base, "base", X.dtype, (s, o), dev)
     if Y is None:
-        Y = torch.empty((s, o), dtype=X.dtype, device=X.device)
+        Y = X.new_empty((s, o))
+        y, ldy = Y.data_ptr(), o
+    else:
+        y, ldy = _matrix(Y, "Y", X.dtype, (s, o), dev)
     if T is None:
-        T = torch.empty((s, r), dtype=torch.float32, device=X.device)
+        T = X.new_empty((s, r), dtype=torch.float32)
+        t = T.data_ptr()
+    else:
+        t = _dense(T, "T", torch.float32, (s, r), dev)
     workspace = _scratch(lora_forward_workspace(s, h, o, r), "lora_forward", workspace, X.device)
-    st = _lib.i8mm_lora_forward(
-        X.data_ptr(), _row_stride(X, "X", X.dtype, X.shape, dev), a, b, _DTYPES[X.dtype], G, r, i, f,
-        *((None, 0) if base is None else (base.data_ptr(), _row_stride(base, "base", X.dtype, (s, o), dev))),
-        s, h, o, Y.data_ptr(), _row_stride(Y, "Y", X.dtype, (s, o), dev), _dense(T, "T", torch.float32, (s, r), dev),
-        workspace.data_ptr(), _stream(X))
+    st = _lib.i8mm_lora_forward(x, ldx, a, b, _DTYPES[X.dtype], G, r, i, f, bp, ldb, s, h, o, y, ldy, t,
+                                workspace.data_ptr(), _raw_stream(dev))
     _check(st, "lora_forward")
     return Y, T
 
@@ -785,64 +804,65 @@ def lora_backward(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, A: torch.T
     X's type, dA fp32 [G, r, h], dB fp32 [G, r, o]; zero for an adapter that
     no row carries). base [s, h] is the gradient that reaches X through the
     projection itself (None: zeros) and may be passed as dX too; dX is None
-    if input_grad is false."""
-    dev = _matrix_of(X, "X", _LORA_TYPES)
-    s, h = X.shape
-    o = B.shape[-1]
-    G, r, (a, b, i, f) = _adapters(A, B, ids, scale, X.dtype, s, h, o, dev)
+    if input_grad is false. A workspace, if given, is a uint8 tensor of
+    lora_backward_workspace(s, h, o, r, G) bytes or more."""
+    dev, s, h, x, ldx = _rows_of(X, _LORA_TYPES)
+    G, r, o, a, b, i, f = _adapters(X, A, B, ids, scale, s, h, dev)
+    dy, lddy = _matrix(dY, "dY", X.dtype, (s, o), dev)
+    t = _dense(T, "T", torch.float32, (s, r), dev)
+    bp = dx = None
+    ldb = lddx = 0
     if not input_grad:
-        dX = base = None
-    elif dX is None:
-        dX = torch.empty((s, h), dtype=X.dtype, device=X.device)
+        dX = None
+    else:
+        if base is not None:
+            bp, ldb = _matrix(base, "base", X.dtype, (s, h), dev)
+        if dX is None:
+            dX = X.new_empty((s, h))
+        dx, lddx = _matrix(dX, "dX", X.dtype, (s, h), dev)
     if dA is None:
-        dA = torch.empty((G, r, h), dtype=torch.float32, device=X.device)
+        dA = X.new_empty((G, r, h), dtype=torch.float32)
     if dB is None:
-        dB = torch.empty((G, r, o), dtype=torch.float32, device=X.device)
+        dB = X.new_empty((G, r, o), dtype=torch.float32)
     workspace = _scratch(lora_backward_workspace(s, h, o, r, G), "lora_backward", workspace, X.device)
-    st = _lib.i8mm_lora_backward(
-        dY.data_ptr(), _row_stride(dY, "dY", X.dtype, (s, o), dev), X.data_ptr(),
-        _row_stride(X, "X", X.dtype, X.shape, dev), _dense(T, "T", torch.float32, (s, r), dev), a, b,
-        _DTYPES[X.dtype], G, r, i, f,
-        *((None, 0) if base is None else (base.data_ptr(), _row_stride(base, "base", X.dtype, (s, h), dev))),
-        s, h, o,
-        *((None, 0) if dX is None else (dX.data_ptr(), _row_stride(dX, "dX", X.dtype, (s, h), dev))),
-        _dense(dA, "dA", torch.float32, (G, r, h), dev), _dense(dB, "dB", torch.float32, (G, r, o), dev),
-        workspace.data_ptr(), _stream(X))
+    st = _lib.i8mm_lora_backward(dy, lddy, x, ldx, t, a, b, _DTYPES[X.dtype], G, r, i, f, bp, ldb, s, h, o, dx, lddx,
+                                 _dense(dA, "dA", torch.float32, (G, r, h), dev),
+                                 _dense(dB, "dB", torch.float32, (G, r, o), dev), workspace.data_ptr(),
+                                 _raw_stream(dev))
     _check(st, "lora_backward")
     return dX, dA, dB
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
-                   workspace: Optional[torch.Tensor] = None, device: Optional[torch.device] = None) -> torch.Tensor:
-    """The global norm N over all gradients (contiguous GPU tensors, each fp16,
-    bf16 or fp32), as fp32 [1] on the GPU, and the gradients times
-    min(1, max_norm / (N + 1e-6)): in place, or into the tensors of `out`
-    (like grads, each of its gradient's type). device is only needed for an
-    empty list."""
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The global norm N over all gradients (contiguous tensors on the current
+    GPU, each fp16, bf16 or fp32), as fp32 [1] on the GPU, and the gradients
+    times min(1, max_norm / (N + 1e-6)): in place, or into the tensors of
+    `out` (like grads, each of its gradient's type)."""
     grads = list(grads)
     n = len(grads)
-    if n == 0:
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    else:
-        for g in grads:
-            _gpu_of(g, "grads", _NORM_TYPES)
-            if not g.is_contiguous():
-                raise ValueError("grads must be contiguous")
-        dev = grads[0].device
+    dev = torch.cuda.current_device()
+    for g in grads:
+        if not isinstance(g, torch.Tensor):
+            raise TypeError("grads must hold torch.Tensors")
+        if g.get_device() != dev or g.dtype not in _DTYPES or not g.is_contiguous():
+            raise ValueError(f"grads must be contiguous fp16, bf16 or fp32 on the current GPU, cuda:{dev} "
+                             f"(got {g.dtype} of strides {g.stride()} on {g.device})")
     outs = None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out must hold {n} tensors (got {len(out)})")
         for t, g in zip(out, grads):
-            _dense(t, "out", g.dtype, g.shape, dev.index)
+            _dense(t, "out", g.dtype, g.shape, dev)
         outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
     numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    workspace = _scratch(_lib.i8mm_clip_grad_norm_workspace_bytes(numels, n), "clip_grad_norm", workspace, dev)
-    total = torch.empty((1,), dtype=torch.float32, device=dev)
+    device = torch.device("cuda", dev)
+    workspace = _scratch(_lib.i8mm_clip_grad_norm_workspace_bytes(numels, n), "clip_grad_norm", workspace, device)
+    total = torch.empty(1, dtype=torch.float32, device=device)
     st = _lib.i8mm_clip_grad_norm(
         (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), outs, numels,
         (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads]), n, max_norm, workspace.data_ptr(),
-        total.data_ptr(), _stream(total))
+        total.data_ptr(), _raw_stream(dev))
     _check(st, "clip_grad_norm")
     return total

@@ -1,5 +1,6 @@
 // Device helpers shared by the kernels around an adapted layer (layer norm,
-// low-rank adapters, gradient clipping): element types and block sums.
+// low-rank adapters, gradient clipping): element types, groups of eight
+// elements and sums over a wavefront.
 #pragma once
 
 #include "device_common.h"
@@ -8,6 +9,8 @@ namespace i8mm {
 namespace {
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef float v8f __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v) { return static_cast<float>(v); }
@@ -16,26 +19,60 @@ __device__ __forceinline__ float to_float(T v) { return static_cast<float>(v); }
 template <typename T>
 __device__ __forceinline__ T from_float(float v) { return static_cast<T>(v); }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Eight neighbouring elements, loaded and stored by one 16-byte access (two
+// for fp32) at any element alignment: global memory is accessed at byte
+// granularity on this target, an unaligned access only touches one more line.
+template <typename T>
+struct Eight {
+    typedef T vec __attribute__((ext_vector_type(8)));
+    vec v;
+
+    // elements [0, n) of p, zeros beyond (n >= 8: all)
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n >= 8) {
+            __builtin_memcpy(&v, p, sizeof(v));
+        } else {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
+            for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k] : static_cast<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int n) const {
+        if (n >= 8) {
+            __builtin_memcpy(p, &v, sizeof(v));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) p[k] = v[k];
+        }
+    }
+    __device__ __forceinline__ float at(int k) const { return to_float<T>(v[k]); }
+    __device__ __forceinline__ void set(int k, float f) { v[k] = from_float<T>(f); }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
-// Sum over a block of NW wavefronts, in every thread; the same order on
-// every call. red: NW floats of LDS, free for reuse when the call returns
-// in every thread.
-template <int NW>
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    v = wave_sum(v);
-    if constexpr (NW == 1) return v;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) t += red[w];
-    __syncthreads();
-    return t;
+// Sum over the wavefront, in every lane. Within 16 lanes the partners come by
+// lane permutes in the adder's own operand path; the swaps of 16- and 32-lane
+// halves are register moves too, so nothing goes through LDS.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<0xb1>(v);     // lanes xor 1
+    v += dpp<0x4e>(v);     // lanes xor 2
+    v += dpp<0x141>(v);    // mirrored within 8
+    v += dpp<0x140>(v);    // mirrored within 16
+    {
+        const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, v),
+                                                        __builtin_bit_cast(unsigned, v), false, false);
+        v = __builtin_bit_cast(float, static_cast<unsigned>(p[0])) +
+            __builtin_bit_cast(float, static_cast<unsigned>(p[1]));
+    }
+    const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v), __builtin_bit_cast(unsigned, v),
+                                                    false, false);
+    return __builtin_bit_cast(float, static_cast<unsigned>(p[0])) +
+           __builtin_bit_cast(float, static_cast<unsigned>(p[1]));
 }
 
 }  // namespace
