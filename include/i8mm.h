@@ -649,7 +649,7 @@ size_t i8mm_clip_grad_norm_workspace_bytes(const int64_t* numels, int64_t n);
  *
  * grads, outs: HOST arrays of n device pointers (outs may be NULL: the
  * gradients are scaled in place; outs[i] may be grads[i]); numels: host
- * array of n element counts (>= 0); types: host array of n i8mm_dtype
+ * array of n element counts (>= 0, below 2^44 in all); types: host array of n i8mm_dtype
  * values, each the type of grads[i] and outs[i]. The arrays are read before
  * the call returns. Pointers need the alignment of their element; the
  * pointer of an empty tensor may be NULL. max_norm: >= 0, +inf for the norm

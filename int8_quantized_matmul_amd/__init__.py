@@ -13,7 +13,9 @@ at Scale" (paper-graph-ui digest), "The Full LLM.int8() Algorithm".
 
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
@@ -833,36 +835,40 @@ def lora_backward(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
+def _tensor_table(tensors, name: str, device: int):
+    """(pointers, element counts, i8mm_dtypes) of contiguous tensors on the
+    device, as host arrays; written as maps, since a model has hundreds."""
+    T = torch.Tensor
+    if not set(map(T.get_device, tensors)) <= {device} or not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous tensors on the current GPU, cuda:{device}")
+    try:
+        types = array.array("i", map(_DTYPES.__getitem__, map(operator.attrgetter("dtype"), tensors)))
+    except KeyError as e:
+        raise ValueError(f"{name} must be fp16, bf16 or fp32 (got {e.args[0]})") from None
+    return array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), types
+
+
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The global norm N over all gradients (contiguous tensors on the current
     GPU, each fp16, bf16 or fp32), as fp32 [1] on the GPU, and the gradients
     times min(1, max_norm / (N + 1e-6)): in place, or into the tensors of
-    `out` (like grads, each of its gradient's type)."""
+    `out`, each of its gradient's size and type."""
     grads = list(grads)
     n = len(grads)
     dev = torch.cuda.current_device()
-    for g in grads:
-        if not isinstance(g, torch.Tensor):
-            raise TypeError("grads must hold torch.Tensors")
-        if g.get_device() != dev or g.dtype not in _DTYPES or not g.is_contiguous():
-            raise ValueError(f"grads must be contiguous fp16, bf16 or fp32 on the current GPU, cuda:{dev} "
-                             f"(got {g.dtype} of strides {g.stride()} on {g.device})")
-    outs = None
-    if out is not None:
-        out = list(out)
-        if len(out) != n:
-            raise ValueError(f"out must hold {n} tensors (got {len(out)})")
-        for t, g in zip(out, grads):
-            _dense(t, "out", g.dtype, g.shape, dev)
-        outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
-    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
     device = torch.device("cuda", dev)
-    workspace = _scratch(_lib.i8mm_clip_grad_norm_workspace_bytes(numels, n), "clip_grad_norm", workspace, device)
+    pointers, numels, types = _tensor_table(grads, "grads", dev)
+    out_pointers = None
+    if out is not None:
+        out_pointers, out_numels, out_types = _tensor_table(list(out), "out", dev)
+        if out_numels != numels or out_types != types:
+            raise ValueError("out must hold a tensor of each gradient's size and type, in their order")
+    at = numels.buffer_info()[0]
+    workspace = _scratch(_lib.i8mm_clip_grad_norm_workspace_bytes(at, n), "clip_grad_norm", workspace, device)
     total = torch.empty(1, dtype=torch.float32, device=device)
-    st = _lib.i8mm_clip_grad_norm(
-        (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), outs, numels,
-        (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads]), n, max_norm, workspace.data_ptr(),
-        total.data_ptr(), _raw_stream(dev))
+    st = _lib.i8mm_clip_grad_norm(pointers.buffer_info()[0], out_pointers.buffer_info()[0] if out_pointers else None,
+                                  at, types.buffer_info()[0], n, max_norm, workspace.data_ptr(), total.data_ptr(),
+                                  _raw_stream(dev))
     _check(st, "clip_grad_norm")
     return total

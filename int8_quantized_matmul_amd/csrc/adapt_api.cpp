@@ -20,7 +20,7 @@ using i8mm::Dtype;
 using i8mm::launched;
 using i8mm::round_up;
 
-constexpr int64_t kMaxElements = int64_t(1) << 46;   // keeps byte counts far from 64-bit overflow
+constexpr int64_t kMaxElements = int64_t(1) << 44;   // of all gradients of a call: chunk counts stay 32-bit
 
 bool valid_type(int t) { return t == I8MM_F16 || t == I8MM_BF16 || t == I8MM_F32; }
 
@@ -152,7 +152,7 @@ size_t i8mm_clip_grad_norm_workspace_bytes(const int64_t* numels, int64_t n) {
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] < 0 || numels[i] > kMaxElements || (total += numels[i]) > kMaxElements) return 0;
     }
-    return static_cast<size_t>(256 + round_up(8 * i8mm::clip_parts(numels, n), 256));
+    return static_cast<size_t>(256 + round_up(8 * i8mm::clip_parts(n), 256));
 }
 
 i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,

@@ -45,6 +45,12 @@ struct Eight {
                 if (k < n) p[k] = v[k];
         }
     }
+    // The same past the caches, for results that are not read again soon.
+    __device__ __forceinline__ void store_through(T* p, int n) const {
+        typedef vec loose __attribute__((aligned(sizeof(T))));
+        if (n >= 8) __builtin_nontemporal_store(v, reinterpret_cast<loose*>(p));
+        else store(p, n);
+    }
     __device__ __forceinline__ float at(int k) const { return to_float<T>(v[k]); }
     __device__ __forceinline__ void set(int k, float f) { v[k] = from_float<T>(f); }
 };

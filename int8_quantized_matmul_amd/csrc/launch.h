@@ -169,9 +169,9 @@ hipError_t launch_lora_backward(const LoraArgs& a, const void* dY, int64_t lddy,
                                 float* dB, void* workspace, hipStream_t stream);
 
 // The norm over all n tensors to *total, and out = min(1, max_norm / norm)
-// in (in place if out is null). `workspace`: 256 bytes, then clip_parts()
-// doubles. The host arrays are read before the call returns.
-int64_t clip_parts(const int64_t* numel, int64_t n);
+// in (in place if out is null). `workspace`: clip_parts(n) doubles. The host
+// arrays are read before the call returns.
+int64_t clip_parts(int64_t n);
 hipError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* numel, const int32_t* types,
                                  int64_t n, float max_norm, void* workspace, float* total, hipStream_t stream);
 
