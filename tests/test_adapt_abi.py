@@ -135,7 +135,7 @@ def test_clip_workspace():
     q = _lib().i8mm_clip_grad_norm_workspace_bytes
     assert q(None, 0) >= 256 and q(None, 1) == 0 and q(None, -1) == 0
     n = (ctypes.c_int64 * 3)(0, 5, 10 ** 9)
-    assert q(n, 3) > q(n, 2) >= 256
+    assert q(n, 3) >= q(n, 2) >= 256
     assert q((ctypes.c_int64 * 2)(1, -1), 2) == 0
 
 
