@@ -24,6 +24,7 @@
 #include "launch.h"
 
 #include "adapt_common.h"
+#include "../../include/i8mm.h"
 
 #include <type_traits>
 
@@ -125,14 +126,16 @@ struct Adapters {
 // and the tokens its columns, both operands come from memory in the layout
 // that the instruction wants, and a token's sums depend on no other token, so
 // rows past the end are read from the last row and their sums dropped. Of the
-// tile's adapters the block takes every `slots`-th.
-template <typename T, int MT, int RT>
-__global__ __launch_bounds__(kThreads) void k_lora_dot(const T* __restrict__ Z, int64_t ldz, const T* __restrict__ M,
-                                                       int64_t G, int r, int len, const int32_t* __restrict__ ids,
-                                                       int64_t s, int tiles, int slots, int splits,
-                                                       float* __restrict__ P) {
+// tile's adapters the block takes every `slots`-th, and up to NA of them in
+// one pass over Z: a tile where one request ends and the next begins costs no
+// second pass.
+template <typename T, int MT, int RT, int NA>
+__global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ Z, int64_t ldz,
+                                                          const T* __restrict__ M, int64_t G, int r, int len,
+                                                          const int32_t* __restrict__ ids, int64_t s, int tiles,
+                                                          int slots, int splits, float* __restrict__ P) {
     constexpr int TOK = 16 * MT;
-    __shared__ v4f join[2][MT * RT][64];
+    __shared__ v4f join[2][MT * RT * NA][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     const int slot = blockIdx.x % slots, tile = blockIdx.x / slots % tiles, part = blockIdx.x / slots / tiles;
     const int64_t first = static_cast<int64_t>(tile) * TOK;
@@ -148,43 +151,43 @@ __global__ __launch_bounds__(kThreads) void k_lora_dot(const T* __restrict__ Z, 
         z[t] = Z + (i < s ? i : s - 1) * ldz + q * 8;
     }
     Adapters<TOK> adapters(ids, first, s, G);
-    if (slot == 0 && wave == 0) {        // rows without an adapter
+    if (slot == 0 && wave == 0 && (~adapters.left & Adapters<TOK>::mask()) != 0) {   // rows without an adapter
         for (int t = 0; t < TOK; ++t) {
             const int64_t i = first + t;
             if ((adapters.left >> t & 1) == 0 && i < s)
                 for (int k = lane; k < r; k += 64) P[i * r + k] = 0.0f;
         }
     }
-    for (int turn = 0; adapters.left; ++turn) {
-        uint64_t tokens;
-        const int64_t g = adapters.next(tokens);
-        if (turn % slots != slot) continue;
-        const T* m[RT];
+    // one pass over Z for N adapters
+    const auto pass = [&](auto count, const int64_t(&g)[NA], const uint64_t(&tokens)[NA]) {
+        constexpr int N = decltype(count)::value, R = RT * N;
+        const T* m[R];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int k = t * 16 + n < r ? t * 16 + n : r - 1;
-            m[t] = M + (g * r + k) * len + q * 8;
+        for (int t = 0; t < R; ++t) {
+            const int k = t % RT * 16 + n;
+            m[t] = M + (g[t / RT] * r + (k < r ? k : r - 1)) * len + q * 8;
         }
-        v4f sum[MT][RT];
+        v4f sum[MT][R];
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int b = 0; b < RT; ++b) sum[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int b = 0; b < R; ++b) sum[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = k0; k < k1; k += 64) {
-            Vec<T> zv[2][MT], mv[2][RT];
+            Vec<T> zv[2][MT], mv[2][R];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t) zv[u][t] = load16(z[t] + k + u * 32);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) mv[u][t] = load16(m[t] + k + u * 32);
+                for (int t = 0; t < R; ++t) mv[u][t] = load16(m[t] + k + u * 32);
             }
+            __builtin_amdgcn_sched_barrier(0);   // all loads in flight before the first sum
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
-                    for (int b = 0; b < RT; ++b) sum[a][b] = mma(mv[u][b], zv[u][a], sum[a][b]);
+                    for (int b = 0; b < R; ++b) sum[a][b] = mma(mv[u][b], zv[u][a], sum[a][b]);
         }
         // wavefronts 2 and 3 to 0 and 1, then 1 to 0
 #pragma unroll
@@ -194,234 +197,432 @@ __global__ __launch_bounds__(kThreads) void k_lora_dot(const T* __restrict__ Z, 
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
-                    for (int b = 0; b < RT; ++b) join[wave - half][a * RT + b][lane] = sum[a][b];
+                    for (int b = 0; b < R; ++b) join[wave - half][a * R + b][lane] = sum[a][b];
             }
             __syncthreads();
             if (wave < half) {
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
-                    for (int b = 0; b < RT; ++b) sum[a][b] += join[wave][a * RT + b][lane];
+                    for (int b = 0; b < R; ++b) sum[a][b] += join[wave][a * R + b][lane];
             }
         }
-        if (wave == 0) {
+        if (wave != 0) return;
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                if ((tokens >> (a * 16 + n) & 1) == 0) continue;
-                float* p = P + (first + a * 16 + n) * r;
+        for (int a = 0; a < MT; ++a) {
+            float* p = P + (first + a * 16 + n) * r;
 #pragma unroll
-                for (int b = 0; b < RT; ++b)
+            for (int b = 0; b < R; ++b) {
+                if ((tokens[b / RT] >> (a * 16 + n) & 1) == 0) continue;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int k = b * 16 + q * 4 + e;
-                        if (k < r) p[k] = sum[a][b][e];
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int k = b % RT * 16 + q * 4 + e;
+                    if (k < r) p[k] = sum[a][b][e];
+                }
             }
+        }
+    };
+    int64_t g[NA];
+    uint64_t tokens[NA];
+    int held = 0;
+    for (int turn = 0; adapters.left; ++turn) {
+        uint64_t mine;
+        const int64_t id = adapters.next(mine);
+        if (turn % slots != slot) continue;
+        if (NA == 2 && held == 0) {
+            g[0] = id;
+            tokens[0] = mine;
+            held = 1;
+        } else {
+            g[NA - 1] = id;
+            tokens[NA - 1] = mine;
+            pass(std::integral_constant<int, NA>(), g, tokens);
+            held = 0;
         }
     }
+    if (NA == 2 && held == 1) pass(std::integral_constant<int, 1>(), g, tokens);
 }
 
 // ---------------------------------------------------------------------------
-// add: out_i = base_i + f_g P_i M_g, with P the sum over the splits, which the
-// blocks of the first columns also write to T.
+// add: out_i = base_i + f_g P_i M_g.
 //
-// A block takes TOK = 16 MT tokens and 512 columns. It first joins the splits
-// of its tokens' P and lays their two parts out in LDS, once for its four
-// wavefronts: [token][16 ranks][first parts, second parts], so that one matrix
-// instruction of 32 products takes 16 ranks with both parts. Each wavefront
-// then takes 128 columns: M's rows are read 16 bytes a lane (eight columns of
-// one rank) and turned in registers, so that the columns are the rows of the
-// matrix instruction. The lane of row m reads the columns from
-// (m % 4 * 4 + m / 4) * 8: a lane's four sums of one instruction then belong
-// to four groups of eight columns 32 apart, and each group leaves as one
-// 16-byte store beside its neighbours'.
+// P enters as two parts side by side, [16 ranks of the first, 16 of the
+// second], so that one matrix instruction of 32 products takes 16 ranks whole.
+// A wavefront takes 128 columns: M's rows are read 16 bytes a lane (eight
+// columns of one rank) and turned in registers, so that the columns are the
+// rows of the matrix instruction and the tokens its columns. The lane of row m
+// reads the columns from (m % 4 * 4 + m / 4) * 8: a lane's four sums of one
+// instruction then belong to four groups of eight columns 32 apart, and each
+// group leaves as one 16-byte store beside its neighbours'.
 constexpr int kAddColumns = kWaves * 128;
 
-template <typename T, int MT>
-__global__ __launch_bounds__(kThreads) void k_lora_add(const float* __restrict__ P, int splits,
-                                                       const T* __restrict__ M, int64_t G, int r, int len,
-                                                       const int32_t* __restrict__ ids,
-                                                       const float* __restrict__ scale, const T* base, int64_t ldb,
-                                                       T* out, int64_t ldo, int64_t s, int slots,
-                                                       float* __restrict__ Tout) {
-    constexpr int TOK = 16 * MT, PER = kThreads / TOK;      // PER threads a token lay out its parts
-    extern __shared__ __align__(16) unsigned char lds[];
-    const int steps = (r + 15) / 16, rp = steps * 16;
-    T* parts = reinterpret_cast<T*>(lds);                               // [TOK][steps][32]
-    float* values = reinterpret_cast<float*>(lds + TOK * rp * 4);       // [TOK][rp + 1]
-    int* exps = reinterpret_cast<int*>(values + TOK * (rp + 1));        // [TOK]
+// Eight operands of 16 columns x 16 ranks (both parts alike) of M's rows
+// [st 16, st 16 + 16): operand j holds column mcol + j of each lane. Ranks
+// past r are 0.
+template <typename T>
+__device__ __forceinline__ void load_ranks(const T* Mg, int64_t len, int r, int st, int q, int mcol,
+                                           Vec<T>(&columns)[8]) {
+    const int k0 = st * 16 + (q & 1) * 8;
+    Vec<T> rows[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        rows[k] = Vec<T>{};
+        if (k0 + k < r) rows[k] = load16(Mg + (k0 + k) * len + mcol);
+    }
+    transpose8<T>(rows, columns);
+}
+
+// f_g 2^-ex, kept finite where f_g is (a sum of 0 has to stay 0).
+__device__ __forceinline__ float factor_of(float f, int ex) {
+    const float v = ldexpf(f, -ex);
+    return fabsf(f) < __builtin_inff() ? fminf(fmaxf(v, -3.4028235e38f), 3.4028235e38f) : v;
+}
+
+// The columns of store e of a lane, and the stores of a token's 128 columns.
+__device__ __forceinline__ int column_of(int c0, int e, int q) { return c0 + e * 32 + q * 8; }
+
+template <typename T>
+__device__ __forceinline__ void store_sums(T* row, int c0, int len, int q, const Vec<T>(&b)[4], const v4f(&sum)[8],
+                                           float factor) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int col = column_of(c0, e, q);
+        Vec<T> y;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(sum[j][e], factor, to_float<T>(b[e][j])));
+        if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = y;
+    }
+}
+
+// Few tokens: a block takes 16 tokens, 512 columns and one of the tile's
+// adapters (slots = 16, so each has its own; a block without one leaves). It
+// joins the splits of its tokens' P itself, while M's first ranks and base are
+// on their way, and its first columns' blocks also write them to T.
+template <typename T>
+__global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __restrict__ P, int splits,
+                                                              const T* __restrict__ M, int64_t G, int r, int len,
+                                                              const int32_t* __restrict__ ids,
+                                                              const float* __restrict__ scale, const T* base,
+                                                              int64_t ldb, T* out, int64_t ldo, int64_t s,
+                                                              float* __restrict__ Tout) {
+    constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
+    __shared__ __align__(16) T parts[16 * kSteps * 32];     // [token][step][32]
+    __shared__ int exps[16];
+    const int steps = (r + 15) / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     const int col_blocks = (len + kAddColumns - 1) / kAddColumns;
-    const int cb = blockIdx.x % col_blocks, slot = blockIdx.x / col_blocks % slots;
-    const int64_t first = static_cast<int64_t>(blockIdx.x / col_blocks / slots) * TOK;
-    Adapters<TOK> adapters(ids, first, s, G);
+    const int cb = blockIdx.x % col_blocks, slot = blockIdx.x / col_blocks % 16;
+    const int64_t first = static_cast<int64_t>(blockIdx.x / col_blocks / 16) * 16;
+    Adapters<16> adapters(ids, first, s, G);
+    const uint64_t none = ~adapters.left & 0xffff;
+    int64_t g = -1;
+    uint64_t tokens = 0;
+    for (int turn = 0; adapters.left; ++turn) {
+        uint64_t mine;
+        const int id = adapters.next(mine);
+        if (turn == slot) {
+            g = id;
+            tokens = mine;
+            break;
+        }
+    }
+    if (g < 0 && slot != 0) return;
+
+    const int c0 = cb * kAddColumns + wave * 128;
+    const int mc = c0 + ((n & 3) * 4 + (n >> 2)) * 8;
+    const int mcol = mc < len ? mc : 0;
+    const T* Mg = M + (g < 0 ? 0 : g) * r * len;
+    Vec<T> columns[8], b[4];
+    if (g >= 0) load_ranks<T>(Mg, len, r, 0, q, mcol, columns);
+    const uint64_t touched = tokens | (slot == 0 ? none : 0);
+    const int64_t i = first + n;
+    const bool here = (touched >> n & 1) && i < s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        b[e] = Vec<T>{};
+        const int col = column_of(c0, e, q);
+        if (base && here && col < len) b[e] = load16(base + i * ldb + col);
+    }
     {
-        const int t = threadIdx.x / PER, sub = threadIdx.x % PER;
-        const int64_t i = first + t;
-        float most = 0.0f;
-        for (int k = sub; k < rp; k += PER) {
-            float v = 0.0f;
-            if (k < r && i < s) {
-                const float* p = P + i * r + k;
-                for (int u = 0; u < splits; ++u) v += p[static_cast<int64_t>(u) * s * r];
-                if (Tout && cb == 0 && slot == 0) Tout[i * r + k] = v;
+        const int t = threadIdx.x / 16, sub = threadIdx.x % 16;
+        const int64_t it = first + t;
+        const bool mine = (touched >> t & 1) && it < s;
+        float v[kSteps], most = 0.0f;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            v[st] = 0.0f;
+            if (st >= steps) continue;
+            const int k = st * 16 + sub;
+            if (mine && k < r) {
+                const float* p = P + it * r + k;
+#pragma unroll 4
+                for (int u = 0; u < splits; ++u) v[st] += p[static_cast<int64_t>(u) * s * r];
+                if (Tout && cb == 0) Tout[it * r + k] = v[st];
             }
-            values[t * (rp + 1) + k] = v;
             // NaN counts as infinity: no power of two for the row
-            most = fmaxf(most, v == v ? fabsf(v) : __builtin_inff());
+            most = fmaxf(most, v[st] == v[st] ? fabsf(v[st]) : __builtin_inff());
         }
 #pragma unroll
-        for (int off = 1; off < PER; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
+        for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
         const int ex = scale_exponent<T>(most);
         if (sub == 0) exps[t] = ex;
-        for (int k = sub; k < rp; k += PER) {
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            if (st >= steps) continue;
             T part[2];
-            split<T, 2>(values[t * (rp + 1) + k], ex, part);
-            T* to = parts + (t * steps + k / 16) * 32 + k % 16;
+            split<T, 2>(v[st], ex, part);
+            T* to = parts + (t * steps + st) * 32 + sub;
             to[0] = part[0];
             to[16] = part[1];
         }
     }
     __syncthreads();
-
-    const int c0 = cb * kAddColumns + wave * 128;           // the wavefront's first column
     if (c0 >= len) return;
-    const int mc = c0 + ((n & 3) * 4 + (n >> 2)) * 8;       // the columns that this lane reads of M
-    const int mcol = mc < len ? mc : c0;
-    const auto write = [&](int64_t i, const v4f(&sum)[8], float factor, int ex) {
+    T* row = out + i * ldo;
+    if (here && (none >> n & 1) && out != base) {            // rows without an adapter are base's
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int col = c0 + e * 32 + q * 8;
-            if (col >= len) continue;
-            Vec<T> b{}, y;
-            if (base) b = load16(base + i * ldb + col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = from_float<T>(to_float<T>(b[j]) + ldexpf(sum[j][e], -ex) * factor);
-            *reinterpret_cast<Vec<T>*>(out + i * ldo + col) = y;
-        }
-    };
-    if (slot == 0 && out != base) {      // rows without an adapter are base's
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-            const int64_t i = first + a * 16 + n;
-            if ((adapters.left >> (a * 16 + n) & 1) == 0 && i < s) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = c0 + e * 32 + q * 8;
-                    if (col >= len) continue;
-                    Vec<T> b{};
-                    if (base) b = load16(base + i * ldb + col);
-                    *reinterpret_cast<Vec<T>*>(out + i * ldo + col) = b;
-                }
-            }
+            const int col = column_of(c0, e, q);
+            if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = b[e];
         }
     }
-    for (int turn = 0; adapters.left; ++turn) {
-        uint64_t tokens;
-        const int64_t g = adapters.next(tokens);
-        if (turn % slots != slot) continue;
-        v4f sum[MT][8];
+    if (g < 0) return;
+    v4f sum[8];
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+    for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int st = 0; st < steps; ++st) {
+        if (st > 0) load_ranks<T>(Mg, len, r, st, q, mcol, columns);
+        const Vec<T> p = load16(parts + (n * steps + st) * 32 + q * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[a][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int st = 0; st < steps; ++st) {
-            const int k0 = st * 16 + (q & 1) * 8;           // this lane's eight ranks, of both parts alike
-            Vec<T> rows[8], columns[8];
+        for (int j = 0; j < 8; ++j) sum[j] = mma(columns[j], p, sum[j]);
+    }
+    if (tokens >> n & 1) store_sums<T>(row, c0, len, q, b, sum, factor_of(scale[g], exps[n]));
+}
+
+// Joins the splits of P for many tokens, 16 lanes a token: T (fp32) and, laid
+// out as add takes them, the two parts: [tile of 16][step][token][32], with
+// the exponent of each token.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, int splits, int r, int64_t s,
+                                                        float* __restrict__ Tout, T* __restrict__ parts,
+                                                        int32_t* __restrict__ exps) {
+    constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
+    const int steps = (r + 15) / 16, t = threadIdx.x / 16, sub = threadIdx.x % 16;
+    const int64_t tile = blockIdx.x, i = tile * 16 + t;
+    float v[kSteps], most = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                rows[k] = Vec<T>{};
-                if (k0 + k < r) rows[k] = load16(M + (g * r + k0 + k) * len + mcol);
-            }
-            transpose8<T>(rows, columns);
+    for (int st = 0; st < kSteps; ++st) {
+        v[st] = 0.0f;
+        const int k = st * 16 + sub;
+        if (i < s && k < r) {
+            const float* p = P + i * r + k;
+#pragma unroll 4
+            for (int u = 0; u < splits; ++u) v[st] += p[static_cast<int64_t>(u) * s * r];
+            if (Tout) Tout[i * r + k] = v[st];
+        }
+        most = fmaxf(most, v[st] == v[st] ? fabsf(v[st]) : __builtin_inff());
+    }
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                const Vec<T> p = load16(parts + ((a * 16 + n) * steps + st) * 32 + q * 8);
+    for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
+    const int ex = scale_exponent<T>(most);
+    if (sub == 0) exps[i] = ex;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[a][j] = mma(columns[j], p, sum[a][j]);
+    for (int st = 0; st < kSteps; ++st) {
+        if (st >= steps) continue;
+        T part[2];
+        split<T, 2>(v[st], ex, part);
+        T* to = parts + ((tile * steps + st) * 16 + t) * 32 + sub;
+        to[0] = part[0];
+        to[16] = part[1];
+    }
+}
+
+// Many tokens: a block takes 512 columns and `run` tiles of 16 tokens one
+// after another, with the next tile's base, parts and ids on their way while
+// this one's sums are formed. Up to 64 ranks (ST steps of 16) M's operands
+// stay in registers for as long as the adapter does not change; beyond (ST =
+// 0) they are read again for each tile.
+template <typename T, int ST>
+__global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restrict__ parts,
+                                                               const int32_t* __restrict__ exps,
+                                                               const T* __restrict__ M, int64_t G, int r, int len,
+                                                               const int32_t* __restrict__ ids,
+                                                               const float* __restrict__ scale, const T* base,
+                                                               int64_t ldb, T* out, int64_t ldo, int64_t s, int tiles,
+                                                               int run) {
+    constexpr int KEEP = ST > 0 ? ST : 1;
+    const int steps = ST > 0 ? ST : (r + 15) / 16;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
+    const int col_blocks = (len + kAddColumns - 1) / kAddColumns;
+    const int c0 = static_cast<int>(blockIdx.x % col_blocks) * kAddColumns + wave * 128;
+    const int t0 = static_cast<int>(blockIdx.x / col_blocks) * run, t1 = t0 + run < tiles ? t0 + run : tiles;
+    if (c0 >= len) return;
+    const int mc = c0 + ((n & 3) * 4 + (n >> 2)) * 8;
+    const int mcol = mc < len ? mc : 0;
+
+    struct Fetched {
+        Vec<T> b[4], p[KEEP];
+        int ex, id;
+    };
+    const auto fetch = [&](int tile, Fetched& f) {
+        const int64_t i = static_cast<int64_t>(tile) * 16 + n, at = i < s ? i : s - 1;
+        f.id = ids[at];
+        if (i >= s || f.id < 0 || f.id >= G) f.id = -1;
+        f.ex = exps[i];
+        if constexpr (ST > 0) {
+#pragma unroll
+            for (int st = 0; st < ST; ++st) f.p[st] = load16(parts + ((static_cast<int64_t>(tile) * ST + st) * 16 + n) * 32 + q * 8);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int col = column_of(c0, e, q);
+            f.b[e] = Vec<T>{};
+            if (base) f.b[e] = load16(base + at * ldb + (col < len ? col : 0));
+        }
+    };
+    int64_t cur = -1;
+    float f = 0.0f;
+    Vec<T> columns[KEEP][8];
+    Fetched next;
+    fetch(t0, next);
+    for (int tile = t0; tile < t1; ++tile) {
+        const Fetched now = next;
+        if (tile + 1 < t1) fetch(tile + 1, next);
+        const int64_t i = static_cast<int64_t>(tile) * 16 + n;
+        T* row = out + i * ldo;
+        uint64_t left = __ballot(now.id >= 0) & 0xffff;
+        if (now.id < 0 && i < s && out != base) {            // rows without an adapter are base's
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = column_of(c0, e, q);
+                if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = now.b[e];
             }
         }
-        const float factor = scale[g];
+        while (left) {
+            const int64_t g = __builtin_amdgcn_readlane(now.id, __builtin_ctzll(left));
+            left &= ~__ballot(now.id == g);
+            const T* Mg = M + g * r * len;
+            if (g != cur) {
+                cur = g;
+                f = scale[g];
+                if constexpr (ST > 0) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
-            if (tokens >> (a * 16 + n) & 1) write(first + a * 16 + n, sum[a], factor, exps[a * 16 + n]);
+                    for (int st = 0; st < ST; ++st) load_ranks<T>(Mg, len, r, st, q, mcol, columns[st]);
+                }
+            }
+            v4f sum[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (ST > 0) {
+#pragma unroll
+                for (int st = 0; st < ST; ++st)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] = mma(columns[st][j], now.p[st], sum[j]);
+            } else {
+                for (int st = 0; st < steps; ++st) {
+                    const Vec<T> p = load16(parts + ((static_cast<int64_t>(tile) * steps + st) * 16 + n) * 32 + q * 8);
+                    load_ranks<T>(Mg, len, r, st, q, mcol, columns[0]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] = mma(columns[0][j], p, sum[j]);
+                }
+            }
+            if (now.id == g) store_sums<T>(row, c0, len, q, now.b, sum, factor_of(f, now.ex));
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
 // grad: the tokens in the order of their adapters, in chunks of up to KC
-// tokens of one adapter.
+// tokens of one adapter, each chunk in tiles of 32.
 
 struct Chunk {
     int32_t g;                       // the adapter, or -1 for an unused entry
     int32_t first;                   // into the ordered tokens
     int32_t count;
-    int32_t tile;                    // first tile of 32 positions in the laid-out factors
+    int32_t tile;                    // the chunk's first tile
     int32_t part;                    // partial sums of the chunk, or -1: the adapter's only one
 };
 
 struct Plan {
-    int32_t* order;                  // [s]: the tokens, by adapter and then by place
+    int32_t* order;                  // [s + 32]: the tokens, by adapter and then by place
     int32_t* count;                  // [G]: tokens of each adapter
     int32_t* part;                   // [G]: its first partial sums
+    int32_t* chunk_of;               // [s]: the chunk of each token that has an adapter
+    int32_t* tile_chunk;             // [tiles]: the chunk of each tile, or -1
     Chunk* chunks;                   // [slots]
-    int slots;
+    uint32_t* most;                  // [2][slots][rank tiles]: largest |factor|, as fp32 bits
+    int slots, tiles, rank_tiles;
 };
 
 constexpr int kPlanThreads = 1024;
 
 // One block an adapter: it counts the tokens of lower adapters (C), how many
 // of those there are (D) and its own (n), then lists its own in order. Its
-// chunks start at entry C / KC + D, its positions at the next multiple of 32
-// from C plus 32 D, its partial sums, if it has more than one chunk, at
-// 2 C / KC: each leaves the adapters room whatever their counts, without one
-// block knowing the others'. Unused entries up to the next adapter's are
-// marked by this one.
+// chunks start at entry C / KC + D, its tiles at C / 32 rounded up plus D, its
+// partial sums, if it has more than one chunk, at 2 C / KC: each leaves the
+// adapters room whatever their counts, without one block knowing the others'.
+// Unused entries up to the next adapter's are marked by this one.
 __global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __restrict__ ids, int s, int G, int KC,
                                                             Plan plan) {
-    __shared__ int wave_counts[kPlanThreads / 64];
+    constexpr int W = kPlanThreads / 64;
+    __shared__ int counts[4][W];
     __shared__ uint32_t seen[2048];
-    __shared__ int totals[4];
-    const int g = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int k = threadIdx.x; k < (G + 31) / 32; k += kPlanThreads) seen[k] = 0;
-    if (threadIdx.x < 4) totals[threadIdx.x] = 0;
+    const int g = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, words = (G + 31) / 32;
+    for (int k = threadIdx.x; k < words; k += kPlanThreads) seen[k] = 0;
     __syncthreads();
     int lower = 0, own = 0, valid = 0;
-    for (int i = threadIdx.x; i < s; i += kPlanThreads) {
-        const int id = ids[i];
-        if (id < 0 || id >= G) continue;
-        ++valid;
-        own += id == g;
-        if (id < g) {
-            ++lower;
-            if ((seen[id >> 5] >> (id & 31) & 1) == 0) atomicOr(&seen[id >> 5], 1u << (id & 31));
-        }
+    for (int i0 = 0; i0 < s; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x, id = i < s ? ids[i] : -1;
+        const bool low = id >= 0 && id < g;
+        valid += __popcll(__ballot(id >= 0 && id < G));
+        own += __popcll(__ballot(id == g));
+        lower += __popcll(__ballot(low));
+        if (low && (seen[id >> 5] >> (id & 31) & 1) == 0) atomicOr(&seen[id >> 5], 1u << (id & 31));
     }
     __syncthreads();
     int distinct = 0;
-    for (int k = threadIdx.x; k < (G + 31) / 32; k += kPlanThreads) distinct += __popc(seen[k]);
-    atomicAdd(&totals[0], lower);        // integers: any order gives the same sum
-    atomicAdd(&totals[1], own);
-    atomicAdd(&totals[2], valid);
-    atomicAdd(&totals[3], distinct);
+    for (int k0 = 0; k0 < words; k0 += kPlanThreads) {
+        const int k = k0 + threadIdx.x;
+        int d = k < words ? __popc(seen[k]) : 0;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off, kWave);
+        distinct += d;
+    }
+    if (lane == 0) {
+        counts[0][wave] = lower;
+        counts[1][wave] = own;
+        counts[2][wave] = valid;
+        counts[3][wave] = distinct;
+    }
     __syncthreads();
-    const int C = totals[0], n = totals[1], D = totals[3];
-    const bool last = C + n == totals[2];
-    const int used = (n + KC - 1) / KC, begin = C / KC + D;
-    const int end = last ? plan.slots : (C + n) / KC + D + 1;
+    int total[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int w = 0; w < W; ++w) total[k] += counts[k][w];
+    const int C = total[0], n = total[1], D = total[3];
+    const bool last = C + n == total[2];
+    const int used = (n + KC - 1) / KC, begin = C / KC + D, part = static_cast<int>(2 * static_cast<int64_t>(C) / KC);
+    const int tile0 = (C + 31) / 32 + D;
     if (threadIdx.x == 0) {
         plan.count[g] = n;
-        plan.part[g] = static_cast<int>(2 * static_cast<int64_t>(C) / KC);
+        plan.part[g] = part;
     }
-    if (n > 0 || (g == 0 && totals[2] == 0)) {
+    if (n > 0 || (g == 0 && total[2] == 0)) {
+        const int end = last ? plan.slots : (C + n) / KC + D + 1;
         for (int k = begin + threadIdx.x; k < end; k += kPlanThreads) {
             const int c = k - begin;
             Chunk e{-1, 0, 0, 0, -1};
             if (c < used)
-                e = Chunk{g, C + c * KC, n - c * KC < KC ? n - c * KC : KC, (C + 31) / 32 + D + c * (KC / 32),
-                          used > 1 ? static_cast<int32_t>(2 * static_cast<int64_t>(C) / KC) + c : -1};
+                e = Chunk{g, C + c * KC, n - c * KC < KC ? n - c * KC : KC, tile0 + c * (KC / 32),
+                          used > 1 ? part + c : -1};
             plan.chunks[k] = e;
         }
+        for (int k = begin * plan.rank_tiles + threadIdx.x; k < end * plan.rank_tiles; k += kPlanThreads)
+            plan.most[k] = plan.most[plan.slots * plan.rank_tiles + k] = 0;
+        const int tile_end = last ? plan.tiles : (C + n + 31) / 32 + D + 1;
+        for (int k = tile0 + threadIdx.x; k < tile_end; k += kPlanThreads)
+            plan.tile_chunk[k] = (k - tile0) * 32 < n ? begin + (k - tile0) * 32 / KC : -1;
     }
     if (n == 0) return;
     int before = C;
@@ -429,29 +630,32 @@ __global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __res
         const int i = i0 + threadIdx.x;
         const bool mine = i < s && ids[i] == g;
         const uint64_t vote = __ballot(mine);
-        if (lane == 0) wave_counts[wave] = __popcll(vote);
+        __syncthreads();
+        if (lane == 0) counts[0][wave] = __popcll(vote);
         __syncthreads();
         int at = before, all = 0;
-        for (int k = 0; k < kPlanThreads / 64; ++k) {
-            if (k < wave) at += wave_counts[k];
-            all += wave_counts[k];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            if (k < wave) at += counts[0][k];
+            all += counts[0][k];
         }
-        if (mine) plan.order[at + __popcll(vote & ((1ull << lane) - 1))] = i;
+        if (mine) {
+            at += __popcll(vote & ((1ull << lane) - 1));
+            plan.order[at] = i;
+            plan.chunk_of[i] = begin + (at - C) / KC;
+        }
         before += all;
-        __syncthreads();
     }
 }
 
-// One of the two gradients: the streamed rows Z, the factors P ([splits][s][r],
-// joined here) and what becomes of them.
+// One of the two gradients: the streamed rows Z, the fp32 factors P [s, r] and
+// what becomes of them.
 struct Side {
     const void* Z;
     int64_t ldz;
     int len;
     const float* P;
-    int splits;
-    void* laid;                      // [tile of 32][RT][parts][16 ranks][32] of the element type
-    int32_t* exps;                   // [slots][RT]
+    void* laid;                      // [tile][rank tile][parts][16 ranks][32] of the element type
     float* out;                      // [G][r][len]
     float* part;                     // [.][r][len]
 };
@@ -459,57 +663,72 @@ struct Side {
 template <typename T>
 constexpr int kParts = kScaled<T> ? 2 : 3;
 
-// Lays f_g P out as the matrix instruction takes it: a block takes one chunk,
-// 16 ranks and one side; a wavefront takes 32 tokens at a time, a lane eight
-// of them for one rank.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const float* __restrict__ scale, int64_t s,
-                                                       int r, Plan plan) {
-    __shared__ float red[kWaves];
-    const Chunk c = plan.chunks[blockIdx.x];
-    if (c.g < 0) return;
-    const Side& side = blockIdx.z == 0 ? x : y;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    const int rt = blockIdx.y, tiles = (r + 15) / 16, k = rt * 16 + n;
-    const int steps = (c.count + 31) / 32;
-    const float f = scale[c.g];
-    const auto value = [&](int p) {
-        float v = 0.0f;
-        if (p < c.count && k < r) {
-            const float* at = side.P + static_cast<int64_t>(plan.order[c.first + p]) * r + k;
-            for (int u = 0; u < side.splits; ++u) v += at[static_cast<int64_t>(u) * s * r];
-            v *= f;
-        }
-        return v;
-    };
-    int ex = 0;
-    if constexpr (kScaled<T>) {
-        float most = 0.0f;
-        for (int st = wave; st < steps; st += kWaves) {
+// The largest |f_g P| of each chunk and rank tile, for both sides: 16 lanes a
+// token, joined within the wavefront where its four tokens share a chunk. The
+// maximum of the bits of non-negative numbers is that of the numbers, in any
+// order. NaN counts as infinity.
+__global__ __launch_bounds__(kThreads) void k_lora_most(const float* __restrict__ Px, const float* __restrict__ Py,
+                                                        const int32_t* __restrict__ ids,
+                                                        const float* __restrict__ scale, int64_t s, int64_t G, int r,
+                                                        Plan plan) {
+    const int sub = threadIdx.x % 16, lane = threadIdx.x & 63;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+    const int id = i < s ? ids[i] : -1;
+    const bool valid = id >= 0 && id < G;
+    const int chunk = valid ? plan.chunk_of[i] : -1;
+    const float f = valid ? scale[id] : 0.0f;
+    const bool alike = __ballot(chunk == __builtin_amdgcn_readfirstlane(chunk)) == ~0ull;
+    for (int side = 0; side < 2; ++side) {
+        const float* P = side == 0 ? Px : Py;
+        for (int rt = 0; rt < plan.rank_tiles; ++rt) {
+            const int k = rt * 16 + sub;
+            float v = valid && k < r ? fabsf(f * P[i * r + k]) : 0.0f;
+            if (v != v) v = __builtin_inff();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = value(st * 32 + q * 8 + e);
-                most = fmaxf(most, v == v ? fabsf(v) : __builtin_inff());
+            for (int off = 1; off < 16; off <<= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+            if (alike) {
+                v = fmaxf(v, __shfl_xor(v, 16, kWave));
+                v = fmaxf(v, __shfl_xor(v, 32, kWave));
             }
+            if (chunk >= 0 && (alike ? lane == 0 : sub == 0))
+                atomicMax(plan.most + (side * plan.slots + chunk) * plan.rank_tiles + rt,
+                          __builtin_bit_cast(uint32_t, v));
         }
-        most = wave_max(most);
-        if (lane == 0) red[wave] = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) most = fmaxf(most, red[w]);
-        ex = scale_exponent<T>(most);
-        if (threadIdx.x == 0) side.exps[static_cast<int64_t>(blockIdx.x) * tiles + rt] = ex;
     }
-    for (int st = wave; st < steps; st += kWaves) {
+}
+
+__device__ __forceinline__ float most_of(const Plan& plan, int side, int chunk, int rt) {
+    return __builtin_bit_cast(float, plan.most[(side * plan.slots + chunk) * plan.rank_tiles + rt]);
+}
+
+// Lays f_g P out as the matrix instruction takes it: a block takes one tile, a
+// wavefront 16 ranks of one side at a time, a lane eight tokens of one rank.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const float* __restrict__ scale, int r,
+                                                       Plan plan) {
+    const int chunk = plan.tile_chunk[blockIdx.x];
+    if (chunk < 0) return;
+    const Chunk c = plan.chunks[chunk];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
+    const float f = scale[c.g];
+    const int p0 = (static_cast<int>(blockIdx.x) - c.tile) * 32 + q * 8;
+    int64_t at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) at[e] = p0 + e < c.count ? static_cast<int64_t>(plan.order[c.first + p0 + e]) * r : -1;
+    for (int task = wave; task < 2 * plan.rank_tiles; task += kWaves) {
+        const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task, k = rt * 16 + n;
+        const float* P = which ? y.P : x.P;
+        const int ex = scale_exponent<T>(most_of(plan, which, chunk, rt));
         Vec<T> out[kParts<T>];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             T part[kParts<T>];
-            split<T, kParts<T>>(value(st * 32 + q * 8 + e), ex, part);
+            split<T, kParts<T>>(at[e] >= 0 && k < r ? f * P[at[e] + k] : 0.0f, ex, part);
 #pragma unroll
             for (int p = 0; p < kParts<T>; ++p) out[p][e] = part[p];
         }
-        T* to = static_cast<T*>(side.laid) + (static_cast<int64_t>(c.tile + st) * tiles + rt) * kParts<T> * 512;
+        T* to = static_cast<T*>(which ? y.laid : x.laid) +
+                (static_cast<int64_t>(blockIdx.x) * plan.rank_tiles + rt) * kParts<T> * 512;
 #pragma unroll
         for (int p = 0; p < kParts<T>; ++p) *reinterpret_cast<Vec<T>*>(to + p * 512 + n * 32 + q * 8) = out[p];
     }
@@ -517,39 +736,59 @@ __global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const flo
 
 // out_g[k, j] = sum over the chunk's tokens of f P[i, k] Z[i, j]: a block
 // takes one chunk, up to RT tiles of 16 ranks and 128 columns of one side, its
-// wavefronts every fourth 32 tokens. Z's rows are read 16 bytes a lane (eight
+// wavefronts every fourth tile. Z's rows are read 16 bytes a lane (eight
 // columns of one token) and turned in registers; the ranks are the rows of
 // the matrix instruction, so a lane ends with eight neighbouring columns of
-// four ranks. Tokens past the end have factors of 0 and rows of 0.
+// four ranks. The next tile's rows, and the tokens of the one after, are on
+// their way while this one's sums are formed. Tokens past the end have factors
+// of 0 and rows of 0.
 template <typename T, int RT>
-__global__ __launch_bounds__(kThreads) void k_lora_grad(Side x, Side y, int r, Plan plan) {
+__global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
     __shared__ v4f join[2][RT * 8][64];
     const int xblocks = (x.len + 127) / 128, yblocks = (y.len + 127) / 128;
-    const int cb = blockIdx.x % (xblocks + yblocks);
-    const Chunk c = plan.chunks[blockIdx.x / (xblocks + yblocks)];
+    const int cb = blockIdx.x % (xblocks + yblocks), chunk = blockIdx.x / (xblocks + yblocks);
+    const Chunk c = plan.chunks[chunk];
     if (c.g < 0) return;
-    const Side& side = cb < xblocks ? x : y;
+    const bool second = cb >= xblocks;
+    const int len = second ? y.len : x.len;
+    const int64_t ldz = second ? y.ldz : x.ldz;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    const int col = (cb < xblocks ? cb : cb - xblocks) * 128 + n * 8;
-    const int tiles = (r + 15) / 16, rt0 = blockIdx.y * RT;
-    const T* Z = static_cast<const T*>(side.Z) + (col < side.len ? col : 0);
-    const T* laid = static_cast<const T*>(side.laid) + n * 32 + q * 8;
-    const int32_t* order = plan.order + c.first;
+    const int col = (second ? cb - xblocks : cb) * 128 + n * 8;
+    const int tiles = plan.rank_tiles, rt0 = blockIdx.y * RT;
+    const T* Z = static_cast<const T*>(second ? y.Z : x.Z) + (col < len ? col : 0);
+    const T* laid = static_cast<const T*>(second ? y.laid : x.laid) + n * 32 + q * 8;
+    const int32_t* order = plan.order + c.first + q * 8;
     v4f sum[RT][8];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int steps = (c.count + 31) / 32;
-    for (int st = wave; st < steps; st += kWaves) {
-        Vec<T> rows[8], columns[8];
+    typedef int v8i __attribute__((ext_vector_type(8)));
+    // the lane's eight tokens of a tile: those past the end are not used
+    const auto tokens_of = [&](int st) {
+        v8i t;
+        __builtin_memcpy(&t, order + (st < steps ? st : steps - 1) * 32, sizeof(t));
+        return t;
+    };
+    const auto rows_of = [&](int st, const v8i& t, Vec<T>(&rows)[8]) {
+        if (st * 32 + 32 <= c.count) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int p = st * 32 + q * 8 + e;
-            rows[e] = Vec<T>{};
-            if (p < c.count) rows[e] = load16(Z + static_cast<int64_t>(order[p]) * side.ldz);
+            for (int e = 0; e < 8; ++e) rows[e] = load16(Z + static_cast<int64_t>(t[e]) * ldz);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                rows[e] = Vec<T>{};
+                if (st * 32 + q * 8 + e < c.count) rows[e] = load16(Z + static_cast<int64_t>(t[e]) * ldz);
+            }
         }
-        Vec<T> f[RT][kParts<T>];
+    };
+    Vec<T> rows[8];
+    v8i ahead = tokens_of(wave);
+    if (wave < steps) rows_of(wave, ahead, rows);
+    ahead = tokens_of(wave + kWaves);
+    for (int st = wave; st < steps; st += kWaves) {
+        Vec<T> f[RT][kParts<T>], columns[8];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -559,6 +798,10 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad(Side x, Side y, int r, P
                     f[t][p] = load16(laid + ((static_cast<int64_t>(c.tile + st) * tiles + rt0 + t) * kParts<T> + p) * 512);
             }
         transpose8<T>(rows, columns);
+        __builtin_amdgcn_sched_barrier(0);
+        if (st + kWaves < steps) rows_of(st + kWaves, ahead, rows);
+        ahead = tokens_of(st + 2 * kWaves);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int p = 0; p < kParts<T>; ++p)
 #pragma unroll
@@ -583,15 +826,13 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad(Side x, Side y, int r, P
                 for (int j = 0; j < 8; ++j) sum[t][j] += join[wave][t * 8 + j][lane];
         }
     }
-    if (wave != 0 || col >= side.len) return;
-    float* out = c.part < 0 ? side.out + static_cast<int64_t>(c.g) * r * side.len
-                            : side.part + static_cast<int64_t>(c.part) * r * side.len;
+    if (wave != 0 || col >= len) return;
+    float* out = c.part < 0 ? (second ? y.out : x.out) + static_cast<int64_t>(c.g) * r * len
+                            : (second ? y.part : x.part) + static_cast<int64_t>(c.part) * r * len;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         if (rt0 + t >= tiles) continue;
-        int ex = 0;
-        if constexpr (kScaled<T>)
-            ex = side.exps[static_cast<int64_t>(blockIdx.x / (xblocks + yblocks)) * tiles + rt0 + t];
+        const int ex = scale_exponent<T>(most_of(plan, second, chunk, rt0 + t));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int k = (rt0 + t) * 16 + q * 4 + e;
@@ -602,7 +843,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad(Side x, Side y, int r, P
                 lo[j] = ldexpf(sum[t][j][e], -ex);
                 hi[j] = ldexpf(sum[t][j + 4][e], -ex);
             }
-            v4f* p = reinterpret_cast<v4f*>(out + static_cast<int64_t>(k) * side.len + col);
+            v4f* p = reinterpret_cast<v4f*>(out + static_cast<int64_t>(k) * len + col);
             p[0] = lo;
             p[1] = hi;
         }
@@ -632,10 +873,10 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad_sum(Side x, Side y, int 
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tokens a tile of dot and add: few tokens most likely carry many adapters, so
-// small tiles, and blocks for each of them.
+// Few tokens most likely carry many adapters: small tiles, with blocks for
+// each adapter of a tile (`slots` of them).
 bool few(int64_t s) { return s <= 256; }
-int slots_for(int64_t s) { return s <= 256 ? 16 : s <= 1024 ? 4 : 1; }
+int slots_for(int64_t s) { return few(s) ? 16 : s <= 1024 ? 4 : 1; }
 
 // Parts that dot splits len into: enough blocks for the chip, while each
 // wavefront keeps at least four steps of 64.
@@ -649,121 +890,165 @@ int dot_splits(int64_t s, int64_t len, int64_t r) {
 template <typename T>
 hipError_t dot(const LoraArgs& a, const void* Z, int64_t ldz, const void* M, int64_t len, float* P,
                hipStream_t stream) {
-    const auto go = [&](auto mt, auto rt) {
-        constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value;
+    const auto go = [&](auto mt, auto rt, auto na) {
+        constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NA = decltype(na)::value;
         const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = slots_for(a.s);
         const int splits = dot_splits(a.s, len, a.r);
-        k_lora_dot<T, MT, RT><<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0,
-                               stream>>>(static_cast<const T*>(Z), ldz, static_cast<const T*>(M), a.G, a.r,
-                                         static_cast<int>(len), a.ids, a.s, tiles, slots, splits, P);
+        k_lora_dot<T, MT, RT, NA><<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0,
+                                   stream>>>(static_cast<const T*>(Z), ldz, static_cast<const T*>(M), a.G, a.r,
+                                             static_cast<int>(len), a.ids, a.s, tiles, slots, splits, P);
     };
     using std::integral_constant;
-    const auto ranks = [&](auto mt) {
-        if (a.r <= 16) go(mt, integral_constant<int, 1>());
-        else if (a.r <= 32) go(mt, integral_constant<int, 2>());
-        else if (a.r <= 64) go(mt, integral_constant<int, 4>());
-    };
-    if (a.r > 64) {
-        if (few(a.s)) go(integral_constant<int, 1>(), integral_constant<int, 8>());
-        else go(integral_constant<int, 2>(), integral_constant<int, 8>());
-    } else if (few(a.s)) {
-        ranks(integral_constant<int, 1>());
-    } else {
-        ranks(integral_constant<int, 4>());
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 8> eight;
+    if (few(a.s)) {                      // a block has at most one adapter
+        if (a.r <= 16) go(one, one, one);
+        else if (a.r <= 32) go(one, two, one);
+        else if (a.r <= 64) go(one, four, one);
+        else go(one, eight, one);
+    } else {                             // as many adapters a pass as the registers hold
+        if (a.r <= 16) go(four, one, two);
+        else if (a.r <= 32) go(four, two, two);
+        else if (a.r <= 64) go(four, four, one);
+        else go(two, eight, one);
     }
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t add(const LoraArgs& a, const float* P, int splits, const void* M, int64_t len, const void* base,
-               int64_t ldb, void* out, int64_t ldo, float* Tout, hipStream_t stream) {
-    const auto go = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value;
-        const int64_t tiles = up(a.s, 16 * MT), rp = up(a.r, 16) * 16;
-        const int slots = slots_for(a.s);
-        const size_t lds = 16 * MT * (rp * 4 + (rp + 1) * 4 + 4);
-        k_lora_add<T, MT><<<static_cast<unsigned>(tiles * slots * up(len, kAddColumns)), kThreads, lds, stream>>>(
-            P, splits, static_cast<const T*>(M), a.G, a.r, static_cast<int>(len), a.ids, a.scale,
-            static_cast<const T*>(base), ldb, static_cast<T*>(out), ldo, a.s, slots, Tout);
+hipError_t add_many(const LoraArgs& a, const void* parts, const int32_t* exps, const void* M, int64_t len,
+                    const void* base, int64_t ldb, void* out, int64_t ldo, hipStream_t stream) {
+    const int64_t col_blocks = up(len, kAddColumns), tiles = up(a.s, 16);
+    const int64_t run = tiles * col_blocks / (6 * kCus) > 1 ? tiles * col_blocks / (6 * kCus) : 1;
+    const auto go = [&](auto st) {
+        k_lora_add_many<T, decltype(st)::value>
+            <<<static_cast<unsigned>(up(tiles, run) * col_blocks), kThreads, 0, stream>>>(
+                static_cast<const T*>(parts), exps, static_cast<const T*>(M), a.G, a.r, static_cast<int>(len), a.ids,
+                a.scale, static_cast<const T*>(base), ldb, static_cast<T*>(out), ldo, a.s, static_cast<int>(tiles),
+                static_cast<int>(run));
     };
-    if (few(a.s)) go(std::integral_constant<int, 1>());
-    else go(std::integral_constant<int, 2>());
+    if (a.r <= 16) go(std::integral_constant<int, 1>());
+    else if (a.r <= 32) go(std::integral_constant<int, 2>());
+    else if (a.r <= 48) go(std::integral_constant<int, 3>());
+    else if (a.r <= 64) go(std::integral_constant<int, 4>());
+    else go(std::integral_constant<int, 0>());
+    return hipGetLastError();
+}
+
+// Places in a workspace, each 256-byte aligned.
+struct Places {
+    size_t at = 0;
+    size_t take(int64_t bytes) {
+        const size_t p = at;
+        at += static_cast<size_t>(up(bytes, 256) * 256);
+        return p;
+    }
+};
+
+// Workspace of a dot and what joins it.
+struct DotPlaces {
+    size_t P, parts, exps;
+    DotPlaces(Places& w, int64_t s, int64_t len, int64_t r) {
+        P = w.take(4 * dot_splits(s, len, r) * s * r);
+        parts = w.take(up(s, 16) * up(r, 16) * 16 * 32 * 2);
+        exps = w.take(4 * up(s, 16) * 16);
+    }
+};
+
+template <typename T>
+hipError_t join(const LoraArgs& a, int splits, const float* P, float* Tout, void* parts, int32_t* exps,
+                hipStream_t stream) {
+    k_lora_join<T><<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(P, splits, a.r, a.s, Tout,
+                                                                               static_cast<T*>(parts), exps);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t forward(const LoraArgs& a, const void* X, int64_t ldx, const void* base, int64_t ldb, void* Y, int64_t ldy,
                    float* Tp, void* workspace, hipStream_t stream) {
+    Places w;
+    const DotPlaces d(w, a.s, a.h, a.r);
+    char* ws = static_cast<char*>(workspace);
+    float* P = reinterpret_cast<float*>(ws + d.P);
     const int splits = dot_splits(a.s, a.h, a.r);
-    float* P = splits == 1 && Tp ? Tp : static_cast<float*>(workspace);
-    const hipError_t e = dot<T>(a, X, ldx, a.A, a.h, P, stream);
+    hipError_t e = dot<T>(a, X, ldx, a.A, a.h, P, stream);
     if (e != hipSuccess) return e;
-    return add<T>(a, P, splits, a.B, a.o, base, ldb, Y, ldy, P == Tp ? nullptr : Tp, stream);
+    if (few(a.s)) {
+        k_lora_add_few<T><<<static_cast<unsigned>(up(a.s, 16) * 16 * up(a.o, kAddColumns)), kThreads, 0, stream>>>(
+            P, splits, static_cast<const T*>(a.B), a.G, a.r, static_cast<int>(a.o), a.ids, a.scale,
+            static_cast<const T*>(base), ldb, static_cast<T*>(Y), ldy, a.s, Tp);
+        return hipGetLastError();
+    }
+    int32_t* exps = reinterpret_cast<int32_t*>(ws + d.exps);
+    if ((e = join<T>(a, splits, P, Tp, ws + d.parts, exps, stream)) != hipSuccess) return e;
+    return add_many<T>(a, ws + d.parts, exps, a.B, a.o, base, ldb, Y, ldy, stream);
 }
 
 // The backward pass's workspace.
 struct Layout {
-    int KC, slots;
-    int64_t tiles, parts;            // tiles of 32 positions; partial sums
-    size_t P, order, count, part, chunks, laid[2], exps[2], sums[2], total;
-};
+    int KC, slots, tiles;
+    size_t dT, order, count, part, chunk_of, tile_chunk, chunks, most, laid[2], sums[2];
+    Places w;
+    DotPlaces d;
 
-Layout layout(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) {
-    Layout l;
-    // chunks as long as still leave about 1024 blocks
-    const int64_t blocks = (up(h, 128) + up(o, 128)) * up(r, 64);
-    const int64_t splits = up(4 * kCus, blocks);
-    const int64_t kc = up(up(s > 0 ? s : 1, splits), 128) * 128;
-    l.KC = static_cast<int>(kc);
-    const int64_t groups = G < s ? G : s, rt = up(r, 16);
-    l.slots = static_cast<int>(s / kc + groups + 1);
-    l.tiles = up(s, 32) + groups + 1;
-    l.parts = kc < s ? 2 * s / kc + 1 : 0;
-    size_t at = 0;
-    const auto take = [&](int64_t bytes) {
-        const size_t p = at;
-        at += static_cast<size_t>(up(bytes, 256) * 256);
-        return p;
-    };
-    l.P = take(4 * dot_splits(s, o, r) * s * r);
-    l.order = take(4 * s);
-    l.count = take(4 * G);
-    l.part = take(4 * G);
-    l.chunks = take(static_cast<int64_t>(sizeof(Chunk)) * l.slots);
-    for (int k = 0; k < 2; ++k) {
-        l.laid[k] = take(l.tiles * rt * 3 * 512 * 2);
-        l.exps[k] = take(4 * l.slots * rt);
-        l.sums[k] = take(4 * l.parts * r * (k == 0 ? h : o));
+    Layout(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) : d(w, s, o, r) {
+        // chunks as long as still leave about 1024 blocks
+        const int64_t blocks = (up(h, 128) + up(o, 128)) * up(r, 64);
+        const int64_t kc = up(up(s > 0 ? s : 1, up(4 * kCus, blocks)), 128) * 128;
+        KC = static_cast<int>(kc);
+        const int64_t groups = G < s ? G : s, rt = up(r, 16);
+        slots = static_cast<int>(s / kc + groups + 1);
+        tiles = static_cast<int>(up(s, 32) + groups + 1);
+        const int64_t parts = kc < s ? 2 * s / kc + 1 : 0;
+        dT = w.take(4 * s * r);
+        order = w.take(4 * (s + 32));
+        count = w.take(4 * G);
+        part = w.take(4 * G);
+        chunk_of = w.take(4 * s);
+        tile_chunk = w.take(4 * tiles);
+        chunks = w.take(static_cast<int64_t>(sizeof(Chunk)) * slots);
+        most = w.take(4 * 2 * slots * rt);
+        for (int k = 0; k < 2; ++k) {
+            laid[k] = w.take(tiles * rt * 3 * 512 * 2);
+            sums[k] = w.take(4 * parts * r * (k == 0 ? h : o));
+        }
     }
-    l.total = at;
-    return l;
-}
+};
 
 template <typename T>
 hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void* X, int64_t ldx, const float* Tp,
                     const void* base, int64_t ldb, void* dX, int64_t lddx, float* dA, float* dB, void* workspace,
                     hipStream_t stream) {
-    const Layout l = layout(a.s, a.h, a.o, a.r, a.G);
+    const Layout l(a.s, a.h, a.o, a.r, a.G);
     char* ws = static_cast<char*>(workspace);
-    const Plan plan{reinterpret_cast<int32_t*>(ws + l.order), reinterpret_cast<int32_t*>(ws + l.count),
-                    reinterpret_cast<int32_t*>(ws + l.part), reinterpret_cast<Chunk*>(ws + l.chunks), l.slots};
-    float* P = reinterpret_cast<float*>(ws + l.P);
-    const int splits = dot_splits(a.s, a.o, a.r);
-    const auto side = [&](int k, const void* Z, int64_t ldz, int64_t len, const float* p, int n, float* out) {
-        return Side{Z, ldz, static_cast<int>(len), p, n, ws + l.laid[k], reinterpret_cast<int32_t*>(ws + l.exps[k]),
-                    out, reinterpret_cast<float*>(ws + l.sums[k])};
-    };
-    const Side x = side(0, X, ldx, a.h, P, splits, dA), y = side(1, dY, lddy, a.o, Tp, 1, dB);
+    const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+    const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const unsigned rt = static_cast<unsigned>(up(a.r, 16)), slots = static_cast<unsigned>(l.slots);
+    const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.chunk_of), ints(l.tile_chunk),
+                    reinterpret_cast<Chunk*>(ws + l.chunks), reinterpret_cast<uint32_t*>(ws + l.most), l.slots,
+                    l.tiles, static_cast<int>(rt)};
+    float* dT = floats(l.dT);
+    const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
+    const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
     const int r = a.r;
     k_lora_plan<<<static_cast<unsigned>(a.G), kPlanThreads, 0, stream>>>(a.ids, static_cast<int>(a.s),
                                                                         static_cast<int>(a.G), l.KC, plan);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.s > 0) {
+        float* P = floats(l.d.P);
         if ((e = dot<T>(a, dY, lddy, a.B, a.o, P, stream)) != hipSuccess) return e;
-        if (dX && (e = add<T>(a, P, splits, a.A, a.h, base, ldb, dX, lddx, nullptr, stream)) != hipSuccess) return e;
-        const unsigned rt = static_cast<unsigned>(up(r, 16)), slots = static_cast<unsigned>(l.slots);
-        k_lora_lay<T><<<dim3(slots, rt, 2), kThreads, 0, stream>>>(x, y, a.scale, a.s, r, plan);
+        if ((e = join<T>(a, dot_splits(a.s, a.o, r), P, dT, ws + l.d.parts, ints(l.d.exps), stream)) != hipSuccess)
+            return e;
+        if (dX && (e = add_many<T>(a, ws + l.d.parts, ints(l.d.exps), a.A, a.h, base, ldb, dX, lddx, stream)) !=
+                      hipSuccess)
+            return e;
+        if constexpr (kScaled<T>)
+            k_lora_most<<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(dT, Tp, a.ids, a.scale, a.s, a.G,
+                                                                                    r, plan);
+        k_lora_lay<T><<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const auto go = [&](auto n) {
             constexpr int RT = decltype(n)::value;
@@ -785,11 +1070,13 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
 }  // namespace
 
 size_t lora_forward_scratch(int64_t s, int64_t h, int64_t, int64_t r) {
-    return 4 * static_cast<size_t>(dot_splits(s, h, r)) * s * r;
+    Places w;
+    DotPlaces(w, s, h, r);
+    return w.at;
 }
 
 size_t lora_backward_scratch(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) {
-    return layout(s, h, o, r, G).total;
+    return Layout(s, h, o, r, G).w.at;
 }
 
 hipError_t launch_lora_forward(const LoraArgs& a, const void* X, int64_t ldx, const void* base, int64_t ldb, void* Y,

@@ -121,7 +121,8 @@ SHAPES = [  # s, h, o, r, G, ids
     (32, 64, 1024, 128, 2, "mixed"), (33, 1024, 64, 5, 5, "runs"), (64, 2048, 640, 16, 24, "mixed"),
     (65, 512, 576, 64, 2, "odd"), (129, 576, 320, 100, 3, "runs"), (300, 768, 704, 8, 4, "runs"),
     (511, 256, 256, 32, 2, "one"), (700, 320, 192, 12, 9, "mixed"), (1030, 128, 64, 127, 1, "odd"),
-    (2100, 64, 128, 4, 300, "mixed"), (260, 4160, 4224, 16, 3, "runs"),
+    (2100, 64, 128, 4, 300, "mixed"), (260, 4160, 4224, 16, 3, "runs"), (400, 1088, 640, 64, 3, "runs"),
+    (330, 320, 2112, 48, 2, "mixed"), (1100, 2048, 1024, 64, 1, "one"),
 ]
 
 
