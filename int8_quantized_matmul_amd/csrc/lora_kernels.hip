@@ -50,6 +50,22 @@ constexpr bool kScaled = std::is_same_v<T, _Float16>;
 template <typename T>
 __device__ __forceinline__ Vec<T> load16(const T* p) { return *reinterpret_cast<const Vec<T>*>(p); }
 
+// Memory serves four neighbouring lanes at a time, at full rate only if they
+// read neighbouring bytes, while the matrix instruction wants neighbouring
+// rows in neighbouring lanes. So a row's four 16-byte pieces are read by lanes
+// 4 row ..+3 and handed on: lane 16 piece + row takes lane 4 row + piece's.
+// (Read where they are wanted, 16 rows of 64 bytes went at 16 bytes a clock
+// and CU, a quarter of the rate.)
+template <typename T>
+__device__ __forceinline__ Vec<T> hand_on(const Vec<T>& v) {
+    const int from = ((threadIdx.x & 15) * 4 + (threadIdx.x >> 4 & 3)) * 4;
+    v4u in = __builtin_bit_cast(v4u, v), out;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        out[k] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(in[k])));
+    return __builtin_bit_cast(Vec<T>, out);
+}
+
 // rows[i][j] -> columns[j][i] of an 8 x 8 block of 16-bit elements
 template <typename T>
 __device__ __forceinline__ void transpose8(const Vec<T>(&rows)[8], Vec<T>(&columns)[8]) {
@@ -123,8 +139,7 @@ struct Adapters {
 // A block takes TOK = 16 MT tokens, all ranks (RT tiles of 16) and one of
 // `splits` parts of len, of which each wavefront takes a quarter; the four
 // sums are joined in LDS. The ranks are the rows of the matrix instruction
-// and the tokens its columns, both operands come from memory in the layout
-// that the instruction wants, and a token's sums depend on no other token, so
+// and the tokens its columns; a token's sums depend on no other token, so
 // rows past the end are read from the last row and their sums dropped. Of the
 // tile's adapters the block takes every `slots`-th, and up to NA of them in
 // one pass over Z: a tile where one request ends and the next begins costs no
@@ -144,11 +159,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (w + 1) / all) * 64;
     P += static_cast<int64_t>(part) * s * r;
 
+    const int lrow = lane >> 2, lpiece = (lane & 3) * 8;     // the row and elements of it that this lane reads
     const T* z[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t i = first + t * 16 + n;
-        z[t] = Z + (i < s ? i : s - 1) * ldz + q * 8;
+        const int64_t i = first + t * 16 + lrow;
+        z[t] = Z + (i < s ? i : s - 1) * ldz + lpiece;
     }
     Adapters<TOK> adapters(ids, first, s, G);
     if (slot == 0 && wave == 0 && (~adapters.left & Adapters<TOK>::mask()) != 0) {   // rows without an adapter
@@ -164,8 +180,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
         const T* m[R];
 #pragma unroll
         for (int t = 0; t < R; ++t) {
-            const int k = t % RT * 16 + n;
-            m[t] = M + (g[t / RT] * r + (k < r ? k : r - 1)) * len + q * 8;
+            const int k = t % RT * 16 + lrow;
+            m[t] = M + (g[t / RT] * r + (k < r ? k : r - 1)) * len + lpiece;
         }
         v4f sum[MT][R];
 #pragma unroll
@@ -183,11 +199,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
             }
             __builtin_amdgcn_sched_barrier(0);   // all loads in flight before the first sum
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) zv[u][t] = hand_on<T>(zv[u][t]);
+#pragma unroll
+                for (int t = 0; t < R; ++t) mv[u][t] = hand_on<T>(mv[u][t]);
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
                     for (int b = 0; b < R; ++b) sum[a][b] = mma(mv[u][b], zv[u][a], sum[a][b]);
+            }
         }
         // wavefronts 2 and 3 to 0 and 1, then 1 to 0
 #pragma unroll
@@ -248,15 +269,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
 //
 // P enters as two parts side by side, [16 ranks of the first, 16 of the
 // second], so that one matrix instruction of 32 products takes 16 ranks whole.
-// A wavefront takes 128 columns: M's rows are read 16 bytes a lane (eight
-// columns of one rank) and turned in registers, so that the columns are the
-// rows of the matrix instruction and the tokens its columns. The lane of row m
-// reads the columns from (m % 4 * 4 + m / 4) * 8: a lane's four sums of one
-// instruction then belong to four groups of eight columns 32 apart, and each
-// group leaves as one 16-byte store beside its neighbours'.
+// The tokens are its rows. A wavefront takes 128 columns: M's rows are read 16
+// bytes a lane (eight columns of one rank) and turned in registers, so that
+// eight instructions cover the columns and a lane ends with eight neighbouring
+// columns of four tokens: base and out are moved 16 bytes a lane, 256 adjacent
+// bytes of a token at a time.
 constexpr int kAddColumns = kWaves * 128;
 
-// Eight operands of 16 columns x 16 ranks (both parts alike) of M's rows
+// Eight operands of 16 ranks (both parts alike) x 16 columns of M's rows
 // [st 16, st 16 + 16): operand j holds column mcol + j of each lane. Ranks
 // past r are 0.
 template <typename T>
@@ -278,19 +298,22 @@ __device__ __forceinline__ float factor_of(float f, int ex) {
     return fabsf(f) < __builtin_inff() ? fminf(fmaxf(v, -3.4028235e38f), 3.4028235e38f) : v;
 }
 
-// The columns of store e of a lane, and the stores of a token's 128 columns.
-__device__ __forceinline__ int column_of(int c0, int e, int q) { return c0 + e * 32 + q * 8; }
-
+// Where a lane's piece of its token e is.
 template <typename T>
-__device__ __forceinline__ void store_sums(T* row, int c0, int len, int q, const Vec<T>(&b)[4], const v4f(&sum)[8],
-                                           float factor) {
+__device__ __forceinline__ T* piece_of(T* base, int64_t first, int q, int e, int64_t ld, int col) {
+    return base + (first + q * 4 + e) * ld + col;
+}
+
+// The tokens of `tokens` (bit k: the tile's token k) among a lane's four.
+template <typename T>
+__device__ __forceinline__ void store_sums(T* out, int64_t first, int64_t ldo, int col, int q, uint64_t tokens,
+                                           const Vec<T>(&b)[4], const v4f(&sum)[8], const float(&factor)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int col = column_of(c0, e, q);
         Vec<T> y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(sum[j][e], factor, to_float<T>(b[e][j])));
-        if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = y;
+        for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(sum[j][e], factor[e], to_float<T>(b[e][j])));
+        if (tokens >> (q * 4 + e) & 1) *reinterpret_cast<Vec<T>*>(piece_of(out, first, q, e, ldo, col)) = y;
     }
 }
 
@@ -306,7 +329,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
                                                               int64_t ldb, T* out, int64_t ldo, int64_t s,
                                                               float* __restrict__ Tout) {
     constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
-    __shared__ __align__(16) T parts[16 * kSteps * 32];     // [token][step][32]
+    __shared__ __align__(16) T parts[16 * kSteps * 32];
     __shared__ int exps[16];
     const int steps = (r + 15) / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
@@ -328,25 +351,22 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
     }
     if (g < 0 && slot != 0) return;
 
-    const int c0 = cb * kAddColumns + wave * 128;
-    const int mc = c0 + ((n & 3) * 4 + (n >> 2)) * 8;
-    const int mcol = mc < len ? mc : 0;
+    const int col = cb * kAddColumns + wave * 128 + n * 8;  // this lane's columns
+    const bool inside = col < len;
+    const int mcol = inside ? col : 0;
     const T* Mg = M + (g < 0 ? 0 : g) * r * len;
     Vec<T> columns[8], b[4];
     if (g >= 0) load_ranks<T>(Mg, len, r, 0, q, mcol, columns);
-    const uint64_t touched = tokens | (slot == 0 ? none : 0);
-    const int64_t i = first + n;
-    const bool here = (touched >> n & 1) && i < s;
+    const uint64_t touched = (tokens | (slot == 0 ? none : 0)) & (s - first < 16 ? (1ull << (s - first)) - 1 : 0xffff);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         b[e] = Vec<T>{};
-        const int col = column_of(c0, e, q);
-        if (base && here && col < len) b[e] = load16(base + i * ldb + col);
+        if (base && inside && (touched >> (q * 4 + e) & 1)) b[e] = load16(piece_of(base, first, q, e, ldb, col));
     }
     {
         const int t = threadIdx.x / 16, sub = threadIdx.x % 16;
         const int64_t it = first + t;
-        const bool mine = (touched >> t & 1) && it < s;
+        const bool mine = touched >> t & 1;
         float v[kSteps], most = 0.0f;
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
@@ -371,20 +391,18 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
             if (st >= steps) continue;
             T part[2];
             split<T, 2>(v[st], ex, part);
-            T* to = parts + (t * steps + st) * 32 + sub;
+            // [step][eight ranks][token]: the lanes of the matrix instruction in order
+            T* to = parts + ((st * 4 + sub / 8) * 16 + t) * 8 + sub % 8;
             to[0] = part[0];
-            to[16] = part[1];
+            to[2 * 16 * 8] = part[1];
         }
     }
     __syncthreads();
-    if (c0 >= len) return;
-    T* row = out + i * ldo;
-    if (here && (none >> n & 1) && out != base) {            // rows without an adapter are base's
+    if (inside && out != base) {         // rows without an adapter are base's
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int col = column_of(c0, e, q);
-            if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = b[e];
-        }
+        for (int e = 0; e < 4; ++e)
+            if (touched & none & 1ull << (q * 4 + e))
+                *reinterpret_cast<Vec<T>*>(piece_of(out, first, q, e, ldo, col)) = b[e];
     }
     if (g < 0) return;
     v4f sum[8];
@@ -392,16 +410,20 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
     for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int st = 0; st < steps; ++st) {
         if (st > 0) load_ranks<T>(Mg, len, r, st, q, mcol, columns);
-        const Vec<T> p = load16(parts + (n * steps + st) * 32 + q * 8);
+        const Vec<T> p = load16(parts + (st * 64 + lane) * 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = mma(columns[j], p, sum[j]);
+        for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[j], sum[j]);
     }
-    if (tokens >> n & 1) store_sums<T>(row, c0, len, q, b, sum, factor_of(scale[g], exps[n]));
+    const float f = scale[g];
+    float factor[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) factor[e] = factor_of(f, exps[q * 4 + e]);
+    if (inside) store_sums<T>(out, first, ldo, col, q, tokens, b, sum, factor);
 }
 
 // Joins the splits of P for many tokens, 16 lanes a token: T (fp32) and, laid
-// out as add takes them, the two parts: [tile of 16][step][token][32], with
-// the exponent of each token.
+// out as add takes them, the two parts: [tile of 16][step][eight ranks of a
+// part][token][8], with the exponent of each token.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, int splits, int r, int64_t s,
                                                         float* __restrict__ Tout, T* __restrict__ parts,
@@ -431,17 +453,18 @@ __global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict_
         if (st >= steps) continue;
         T part[2];
         split<T, 2>(v[st], ex, part);
-        T* to = parts + ((tile * steps + st) * 16 + t) * 32 + sub;
+        T* to = parts + (((tile * steps + st) * 4 + sub / 8) * 16 + t) * 8 + sub % 8;
         to[0] = part[0];
-        to[16] = part[1];
+        to[2 * 16 * 8] = part[1];
     }
 }
 
 // Many tokens: a block takes 512 columns and `run` tiles of 16 tokens one
 // after another, with the next tile's base, parts and ids on their way while
-// this one's sums are formed. Up to 64 ranks (ST steps of 16) M's operands
-// stay in registers for as long as the adapter does not change; beyond (ST =
-// 0) they are read again for each tile.
+// this one's sums are formed. M's operands stay for as long as the adapter
+// does not change: up to 32 ranks (ST steps of 16) in registers, up to 64 in
+// LDS, each wavefront its own. Beyond (ST = 0) they are read again for each
+// tile.
 template <typename T, int ST>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restrict__ parts,
                                                                const int32_t* __restrict__ exps,
@@ -450,34 +473,39 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restri
                                                                const float* __restrict__ scale, const T* base,
                                                                int64_t ldb, T* out, int64_t ldo, int64_t s, int tiles,
                                                                int run) {
-    constexpr int KEEP = ST > 0 ? ST : 1;
+    constexpr bool LDS = ST > 2;
+    constexpr int KEEP = LDS || ST == 0 ? 1 : ST;
+    __shared__ Vec<T> held[LDS ? kWaves * ST * 8 * 32 : 1];
     const int steps = ST > 0 ? ST : (r + 15) / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     const int col_blocks = (len + kAddColumns - 1) / kAddColumns;
     const int c0 = static_cast<int>(blockIdx.x % col_blocks) * kAddColumns + wave * 128;
     const int t0 = static_cast<int>(blockIdx.x / col_blocks) * run, t1 = t0 + run < tiles ? t0 + run : tiles;
     if (c0 >= len) return;
-    const int mc = c0 + ((n & 3) * 4 + (n >> 2)) * 8;
-    const int mcol = mc < len ? mc : 0;
+    const int col = c0 + n * 8;                             // this lane's columns
+    const bool inside = col < len;
+    const int mcol = inside ? col : c0;
 
+    // operand j of step st: lanes of equal n and q % 2 hold the same ranks
+    Vec<T>* const mine = held + (LDS ? wave * ST * 8 * 32 + (q & 1) * 16 + n : 0);
     struct Fetched {
-        Vec<T> b[4], p[KEEP];
-        int ex, id;
+        Vec<T> b[4], p[ST > 0 ? ST : 1];
+        v4i ex;
+        int id;
     };
     const auto fetch = [&](int tile, Fetched& f) {
-        const int64_t i = static_cast<int64_t>(tile) * 16 + n, at = i < s ? i : s - 1;
-        f.id = ids[at];
-        if (i >= s || f.id < 0 || f.id >= G) f.id = -1;
-        f.ex = exps[i];
+        const int64_t first = static_cast<int64_t>(tile) * 16, i = first + n;
+        f.id = i < s ? ids[i] : -1;
+        if (f.id >= G) f.id = -1;
+        f.ex = *reinterpret_cast<const v4i*>(exps + first + q * 4);
         if constexpr (ST > 0) {
 #pragma unroll
-            for (int st = 0; st < ST; ++st) f.p[st] = load16(parts + ((static_cast<int64_t>(tile) * ST + st) * 16 + n) * 32 + q * 8);
+            for (int st = 0; st < ST; ++st) f.p[st] = load16(parts + ((static_cast<int64_t>(tile) * ST + st) * 64 + lane) * 8);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int col = column_of(c0, e, q);
             f.b[e] = Vec<T>{};
-            if (base) f.b[e] = load16(base + at * ldb + (col < len ? col : 0));
+            if (base) f.b[e] = load16(base + (first + q * 4 + e < s ? first + q * 4 + e : s - 1) * ldb + mcol);
         }
     };
     int64_t cur = -1;
@@ -488,24 +516,30 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restri
     for (int tile = t0; tile < t1; ++tile) {
         const Fetched now = next;
         if (tile + 1 < t1) fetch(tile + 1, next);
-        const int64_t i = static_cast<int64_t>(tile) * 16 + n;
-        T* row = out + i * ldo;
+        const int64_t first = static_cast<int64_t>(tile) * 16;
         uint64_t left = __ballot(now.id >= 0) & 0xffff;
-        if (now.id < 0 && i < s && out != base) {            // rows without an adapter are base's
+        const uint64_t none = ~left & (s - first < 16 ? (1ull << (s - first)) - 1 : 0xffff);
+        if (none && out != base && inside) {                 // rows without an adapter are base's
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = column_of(c0, e, q);
-                if (col < len) *reinterpret_cast<Vec<T>*>(row + col) = now.b[e];
-            }
+            for (int e = 0; e < 4; ++e)
+                if (none >> (q * 4 + e) & 1)
+                    *reinterpret_cast<Vec<T>*>(piece_of(out, first, q, e, ldo, col)) = now.b[e];
         }
         while (left) {
             const int64_t g = __builtin_amdgcn_readlane(now.id, __builtin_ctzll(left));
-            left &= ~__ballot(now.id == g);
+            const uint64_t tokens = __ballot(now.id == g) & left;
+            left &= ~tokens;
             const T* Mg = M + g * r * len;
             if (g != cur) {
                 cur = g;
                 f = scale[g];
-                if constexpr (ST > 0) {
+                if constexpr (LDS) {
+                    for (int st = 0; st < ST; ++st) {
+                        load_ranks<T>(Mg, len, r, st, q, mcol, columns[0]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) mine[(st * 8 + j) * 32] = columns[0][j];
+                    }
+                } else if constexpr (ST > 0) {
 #pragma unroll
                     for (int st = 0; st < ST; ++st) load_ranks<T>(Mg, len, r, st, q, mcol, columns[st]);
                 }
@@ -513,20 +547,28 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restri
             v4f sum[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (ST > 0) {
+            if constexpr (LDS) {
 #pragma unroll
                 for (int st = 0; st < ST; ++st)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] = mma(columns[st][j], now.p[st], sum[j]);
+                    for (int j = 0; j < 8; ++j) sum[j] = mma(now.p[st], mine[(st * 8 + j) * 32], sum[j]);
+            } else if constexpr (ST > 0) {
+#pragma unroll
+                for (int st = 0; st < ST; ++st)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] = mma(now.p[st], columns[st][j], sum[j]);
             } else {
                 for (int st = 0; st < steps; ++st) {
-                    const Vec<T> p = load16(parts + ((static_cast<int64_t>(tile) * steps + st) * 16 + n) * 32 + q * 8);
+                    const Vec<T> p = load16(parts + ((static_cast<int64_t>(tile) * steps + st) * 64 + lane) * 8);
                     load_ranks<T>(Mg, len, r, st, q, mcol, columns[0]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] = mma(columns[0][j], p, sum[j]);
+                    for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[0][j], sum[j]);
                 }
             }
-            if (now.id == g) store_sums<T>(row, c0, len, q, now.b, sum, factor_of(f, now.ex));
+            float factor[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) factor[e] = factor_of(f, now.ex[e]);
+            if (inside) store_sums<T>(out, first, ldo, col, q, tokens, now.b, sum, factor);
         }
     }
 }
@@ -547,7 +589,6 @@ struct Plan {
     int32_t* order;                  // [s + 32]: the tokens, by adapter and then by place
     int32_t* count;                  // [G]: tokens of each adapter
     int32_t* part;                   // [G]: its first partial sums
-    int32_t* chunk_of;               // [s]: the chunk of each token that has an adapter
     int32_t* tile_chunk;             // [tiles]: the chunk of each tile, or -1
     Chunk* chunks;                   // [slots]
     uint32_t* most;                  // [2][slots][rank tiles]: largest |factor|, as fp32 bits
@@ -639,11 +680,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __res
             if (k < wave) at += counts[0][k];
             all += counts[0][k];
         }
-        if (mine) {
-            at += __popcll(vote & ((1ull << lane) - 1));
-            plan.order[at] = i;
-            plan.chunk_of[i] = begin + (at - C) / KC;
-        }
+        if (mine) plan.order[at + __popcll(vote & ((1ull << lane) - 1))] = i;
         before += all;
     }
 }
@@ -655,7 +692,7 @@ struct Side {
     int64_t ldz;
     int len;
     const float* P;
-    void* laid;                      // [tile][rank tile][parts][16 ranks][32] of the element type
+    void* laid;                      // [tile][rank tile][parts][lane][8] of the element type
     float* out;                      // [G][r][len]
     float* part;                     // [.][r][len]
 };
@@ -663,37 +700,45 @@ struct Side {
 template <typename T>
 constexpr int kParts = kScaled<T> ? 2 : 3;
 
-// The largest |f_g P| of each chunk and rank tile, for both sides: 16 lanes a
-// token, joined within the wavefront where its four tokens share a chunk. The
-// maximum of the bits of non-negative numbers is that of the numbers, in any
-// order. NaN counts as infinity.
-__global__ __launch_bounds__(kThreads) void k_lora_most(const float* __restrict__ Px, const float* __restrict__ Py,
-                                                        const int32_t* __restrict__ ids,
-                                                        const float* __restrict__ scale, int64_t s, int64_t G, int r,
-                                                        Plan plan) {
-    const int sub = threadIdx.x % 16, lane = threadIdx.x & 63;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
-    const int id = i < s ? ids[i] : -1;
-    const bool valid = id >= 0 && id < G;
-    const int chunk = valid ? plan.chunk_of[i] : -1;
-    const float f = valid ? scale[id] : 0.0f;
-    const bool alike = __ballot(chunk == __builtin_amdgcn_readfirstlane(chunk)) == ~0ull;
-    for (int side = 0; side < 2; ++side) {
-        const float* P = side == 0 ? Px : Py;
-        for (int rt = 0; rt < plan.rank_tiles; ++rt) {
-            const int k = rt * 16 + sub;
-            float v = valid && k < r ? fabsf(f * P[i * r + k]) : 0.0f;
-            if (v != v) v = __builtin_inff();
+// The factors f_g P of a tile of 32 ordered tokens: a lane's eight tokens of
+// one rank. Tokens past the chunk's end and ranks past r are 0.
+struct TileFactors {
+    float f;
+    int64_t at[8];                   // the tokens' rows in P, or -1
+
+    __device__ __forceinline__ TileFactors(const Plan& plan, const Chunk& c, const float* scale, int r) {
+        const int p0 = (static_cast<int>(blockIdx.x) - c.tile) * 32 + (threadIdx.x >> 4 & 3) * 8;
+        f = scale[c.g];
 #pragma unroll
-            for (int off = 1; off < 16; off <<= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-            if (alike) {
-                v = fmaxf(v, __shfl_xor(v, 16, kWave));
-                v = fmaxf(v, __shfl_xor(v, 32, kWave));
-            }
-            if (chunk >= 0 && (alike ? lane == 0 : sub == 0))
-                atomicMax(plan.most + (side * plan.slots + chunk) * plan.rank_tiles + rt,
-                          __builtin_bit_cast(uint32_t, v));
-        }
+        for (int e = 0; e < 8; ++e)
+            at[e] = p0 + e < c.count ? static_cast<int64_t>(plan.order[c.first + p0 + e]) * r : -1;
+    }
+    __device__ __forceinline__ void load(const float* P, int k, int r, float(&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = at[e] >= 0 && k < r ? f * P[at[e] + k] : 0.0f;
+    }
+};
+
+// The largest |f_g P| of each chunk and rank tile, for both sides: a block
+// takes one tile, a wavefront one rank tile of one side at a time. The maximum
+// of the bits of non-negative numbers is that of the numbers, in any order.
+// NaN counts as infinity.
+__global__ __launch_bounds__(kThreads) void k_lora_most(Side x, Side y, const float* __restrict__ scale, int r,
+                                                        Plan plan) {
+    const int chunk = plan.tile_chunk[blockIdx.x];
+    if (chunk < 0) return;
+    const TileFactors t(plan, plan.chunks[chunk], scale, r);
+    const int lane = threadIdx.x & 63;
+    for (int task = threadIdx.x >> 6; task < 2 * plan.rank_tiles; task += kWaves) {
+        const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
+        float v[8], most = 0.0f;
+        t.load(which ? y.P : x.P, rt * 16 + (lane & 15), r, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, v[e] == v[e] ? fabsf(v[e]) : __builtin_inff());
+        most = wave_max(most);
+        if (lane == 0)
+            atomicMax(plan.most + (which * plan.slots + chunk) * plan.rank_tiles + rt,
+                      __builtin_bit_cast(uint32_t, most));
     }
 }
 
@@ -708,43 +753,41 @@ __global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const flo
                                                        Plan plan) {
     const int chunk = plan.tile_chunk[blockIdx.x];
     if (chunk < 0) return;
-    const Chunk c = plan.chunks[chunk];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    const float f = scale[c.g];
-    const int p0 = (static_cast<int>(blockIdx.x) - c.tile) * 32 + q * 8;
-    int64_t at[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) at[e] = p0 + e < c.count ? static_cast<int64_t>(plan.order[c.first + p0 + e]) * r : -1;
-    for (int task = wave; task < 2 * plan.rank_tiles; task += kWaves) {
-        const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task, k = rt * 16 + n;
-        const float* P = which ? y.P : x.P;
+    const TileFactors t(plan, plan.chunks[chunk], scale, r);
+    const int lane = threadIdx.x & 63, n = lane & 15;
+    for (int task = threadIdx.x >> 6; task < 2 * plan.rank_tiles; task += kWaves) {
+        const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
         const int ex = scale_exponent<T>(most_of(plan, which, chunk, rt));
+        float v[8];
+        t.load(which ? y.P : x.P, rt * 16 + n, r, v);
         Vec<T> out[kParts<T>];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             T part[kParts<T>];
-            split<T, kParts<T>>(at[e] >= 0 && k < r ? f * P[at[e] + k] : 0.0f, ex, part);
+            split<T, kParts<T>>(v[e], ex, part);
 #pragma unroll
             for (int p = 0; p < kParts<T>; ++p) out[p][e] = part[p];
         }
         T* to = static_cast<T*>(which ? y.laid : x.laid) +
                 (static_cast<int64_t>(blockIdx.x) * plan.rank_tiles + rt) * kParts<T> * 512;
 #pragma unroll
-        for (int p = 0; p < kParts<T>; ++p) *reinterpret_cast<Vec<T>*>(to + p * 512 + n * 32 + q * 8) = out[p];
+        for (int p = 0; p < kParts<T>; ++p) *reinterpret_cast<Vec<T>*>(to + p * 512 + lane * 8) = out[p];
     }
 }
 
 // out_g[k, j] = sum over the chunk's tokens of f P[i, k] Z[i, j]: a block
-// takes one chunk, up to RT tiles of 16 ranks and 128 columns of one side, its
-// wavefronts every fourth tile. Z's rows are read 16 bytes a lane (eight
+// takes one chunk and 128 columns of one side; of its wavefronts, WK share the
+// chunk's tiles and the others take further RT tiles of 16 ranks over the same
+// rows. Z's rows are read 16 bytes a lane (eight
 // columns of one token) and turned in registers; the ranks are the rows of
 // the matrix instruction, so a lane ends with eight neighbouring columns of
 // four ranks. The next tile's rows, and the tokens of the one after, are on
 // their way while this one's sums are formed. Tokens past the end have factors
 // of 0 and rows of 0.
-template <typename T, int RT>
+template <typename T, int RT, int WK>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
-    __shared__ v4f join[2][RT * 8][64];
+    constexpr int WR = kWaves / WK;
+    __shared__ v4f join[WK / 2][WR][RT * 8][64];
     const int xblocks = (x.len + 127) / 128, yblocks = (y.len + 127) / 128;
     const int cb = blockIdx.x % (xblocks + yblocks), chunk = blockIdx.x / (xblocks + yblocks);
     const Chunk c = plan.chunks[chunk];
@@ -754,9 +797,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
     const int64_t ldz = second ? y.ldz : x.ldz;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     const int col = (second ? cb - xblocks : cb) * 128 + n * 8;
-    const int tiles = plan.rank_tiles, rt0 = blockIdx.y * RT;
+    const int wk = wave % WK, wr = wave / WK, tiles = plan.rank_tiles, rt0 = (blockIdx.y * WR + wr) * RT;
     const T* Z = static_cast<const T*>(second ? y.Z : x.Z) + (col < len ? col : 0);
-    const T* laid = static_cast<const T*>(second ? y.laid : x.laid) + n * 32 + q * 8;
+    const T* laid = static_cast<const T*>(second ? y.laid : x.laid) + lane * 8;
     const int32_t* order = plan.order + c.first + q * 8;
     v4f sum[RT][8];
 #pragma unroll
@@ -784,10 +827,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
         }
     };
     Vec<T> rows[8];
-    v8i ahead = tokens_of(wave);
-    if (wave < steps) rows_of(wave, ahead, rows);
-    ahead = tokens_of(wave + kWaves);
-    for (int st = wave; st < steps; st += kWaves) {
+    v8i ahead = tokens_of(wk);
+    if (wk < steps) rows_of(wk, ahead, rows);
+    ahead = tokens_of(wk + WK);
+    for (int st = wk; st < steps; st += WK) {
         Vec<T> f[RT][kParts<T>], columns[8];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -799,8 +842,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
             }
         transpose8<T>(rows, columns);
         __builtin_amdgcn_sched_barrier(0);
-        if (st + kWaves < steps) rows_of(st + kWaves, ahead, rows);
-        ahead = tokens_of(st + 2 * kWaves);
+        if (st + WK < steps) rows_of(st + WK, ahead, rows);
+        ahead = tokens_of(st + 2 * WK);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int p = 0; p < kParts<T>; ++p)
@@ -810,23 +853,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
                 for (int j = 0; j < 8; ++j) sum[t][j] = mma(f[t][p], columns[j], sum[t][j]);
     }
 #pragma unroll
-    for (int half = 2; half >= 1; half /= 2) {
+    for (int half = WK / 2; half >= 1; half /= 2) {
         __syncthreads();
-        if (wave >= half && wave < 2 * half) {
+        if (wk >= half && wk < 2 * half) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) join[wave - half][t * 8 + j][lane] = sum[t][j];
+                for (int j = 0; j < 8; ++j) join[wk - half][wr][t * 8 + j][lane] = sum[t][j];
         }
         __syncthreads();
-        if (wave < half) {
+        if (wk < half) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[t][j] += join[wave][t * 8 + j][lane];
+                for (int j = 0; j < 8; ++j) sum[t][j] += join[wk][wr][t * 8 + j][lane];
         }
     }
-    if (wave != 0 || col >= len) return;
+    if (wk != 0 || col >= len) return;
     float* out = c.part < 0 ? (second ? y.out : x.out) + static_cast<int64_t>(c.g) * r * len
                             : (second ? y.part : x.part) + static_cast<int64_t>(c.part) * r * len;
 #pragma unroll
@@ -874,9 +917,12 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad_sum(Side x, Side y, int 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Few tokens most likely carry many adapters: small tiles, with blocks for
-// each adapter of a tile (`slots` of them).
+// each adapter of a tile. With many, most tiles have one: where a pass does
+// not take two of them, the second has a block of its own, which leaves at
+// once in all other tiles (4096 x 36864, rank 64, two adapters that meet
+// inside a tile: 145 us for the one block's two passes, 95 for two blocks).
 bool few(int64_t s) { return s <= 256; }
-int slots_for(int64_t s) { return few(s) ? 16 : s <= 1024 ? 4 : 1; }
+int slots_for(int64_t s, int64_t r) { return few(s) ? 16 : s <= 1024 ? 4 : r > 32 ? 2 : 1; }
 
 // Parts that dot splits len into: enough blocks for the chip, while each
 // wavefront keeps at least four steps of 64.
@@ -892,7 +938,7 @@ hipError_t dot(const LoraArgs& a, const void* Z, int64_t ldz, const void* M, int
                hipStream_t stream) {
     const auto go = [&](auto mt, auto rt, auto na) {
         constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NA = decltype(na)::value;
-        const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = slots_for(a.s);
+        const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = slots_for(a.s, a.r);
         const int splits = dot_splits(a.s, len, a.r);
         k_lora_dot<T, MT, RT, NA><<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0,
                                    stream>>>(static_cast<const T*>(Z), ldz, static_cast<const T*>(M), a.G, a.r,
@@ -989,7 +1035,7 @@ hipError_t forward(const LoraArgs& a, const void* X, int64_t ldx, const void* ba
 // The backward pass's workspace.
 struct Layout {
     int KC, slots, tiles;
-    size_t dT, order, count, part, chunk_of, tile_chunk, chunks, most, laid[2], sums[2];
+    size_t dT, order, count, part, tile_chunk, chunks, most, laid[2], sums[2];
     Places w;
     DotPlaces d;
 
@@ -1006,7 +1052,6 @@ struct Layout {
         order = w.take(4 * (s + 32));
         count = w.take(4 * G);
         part = w.take(4 * G);
-        chunk_of = w.take(4 * s);
         tile_chunk = w.take(4 * tiles);
         chunks = w.take(static_cast<int64_t>(sizeof(Chunk)) * slots);
         most = w.take(4 * 2 * slots * rt);
@@ -1026,7 +1071,7 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const unsigned rt = static_cast<unsigned>(up(a.r, 16)), slots = static_cast<unsigned>(l.slots);
-    const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.chunk_of), ints(l.tile_chunk),
+    const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
                     reinterpret_cast<Chunk*>(ws + l.chunks), reinterpret_cast<uint32_t*>(ws + l.most), l.slots,
                     l.tiles, static_cast<int>(rt)};
     float* dT = floats(l.dT);
@@ -1046,19 +1091,20 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
                       hipSuccess)
             return e;
         if constexpr (kScaled<T>)
-            k_lora_most<<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(dT, Tp, a.ids, a.scale, a.s, a.G,
-                                                                                    r, plan);
+            k_lora_most<<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         k_lora_lay<T><<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        const auto go = [&](auto n) {
-            constexpr int RT = decltype(n)::value;
+        const auto go = [&](auto n, auto wk) {
+            constexpr int RT = decltype(n)::value, WK = decltype(wk)::value;
             const unsigned blocks = static_cast<unsigned>(up(a.h, 128) + up(a.o, 128));
-            k_lora_grad<T, RT><<<dim3(slots * blocks, static_cast<unsigned>(up(rt, RT))), kThreads, 0, stream>>>(
-                x, y, r, plan);
+            k_lora_grad<T, RT, WK>
+                <<<dim3(slots * blocks, static_cast<unsigned>(up(rt, RT * (kWaves / WK)))), kThreads, 0, stream>>>(
+                    x, y, r, plan);
         };
-        if (rt == 1) go(std::integral_constant<int, 1>());
-        else if (rt == 2) go(std::integral_constant<int, 2>());
-        else go(std::integral_constant<int, 4>());
+        using std::integral_constant;
+        if (rt == 1) go(integral_constant<int, 1>(), integral_constant<int, 4>());
+        else if (rt == 2) go(integral_constant<int, 2>(), integral_constant<int, 4>());
+        else go(integral_constant<int, 2>(), integral_constant<int, 2>());
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t fours = static_cast<int64_t>(r) * (a.h + a.o) / 4;
