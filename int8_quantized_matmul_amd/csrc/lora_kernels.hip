@@ -152,7 +152,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     constexpr int TOK = 16 * MT;
     __shared__ v4f join[2][MT * RT * NA][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    const int slot = blockIdx.x % slots, tile = blockIdx.x / slots % tiles, part = blockIdx.x / slots / tiles;
+    // Neighbouring blocks go to different XCDs, so a slot's blocks are neighbours:
+    // most of the higher slots' have nothing to do. With many tokens those few
+    // start first, since they end last.
+    const int tile = blockIdx.x % tiles, part = blockIdx.x / tiles % splits;
+    const int turn0 = blockIdx.x / tiles / splits, slot = MT == 1 ? turn0 : slots - 1 - turn0;
     const int64_t first = static_cast<int64_t>(tile) * TOK;
     const int steps = len / 64, w = part * kWaves + wave, all = splits * kWaves;
     const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w / all) * 64;
@@ -188,27 +192,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < R; ++b) sum[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        Vec<T> zn[2][MT], mn[2][R];      // the step on its way
+        const auto fetch = [&](int k) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) zn[u][t] = load16(z[t] + k + u * 32);
+#pragma unroll
+                for (int t = 0; t < R; ++t) mn[u][t] = load16(m[t] + k + u * 32);
+            }
+        };
+        if (k0 < k1) fetch(k0);
         for (int k = k0; k < k1; k += 64) {
             Vec<T> zv[2][MT], mv[2][R];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int t = 0; t < MT; ++t) zv[u][t] = load16(z[t] + k + u * 32);
+                for (int t = 0; t < MT; ++t) zv[u][t] = hand_on<T>(zn[u][t]);
 #pragma unroll
-                for (int t = 0; t < R; ++t) mv[u][t] = load16(m[t] + k + u * 32);
+                for (int t = 0; t < R; ++t) mv[u][t] = hand_on<T>(mn[u][t]);
             }
-            __builtin_amdgcn_sched_barrier(0);   // all loads in flight before the first sum
+            __builtin_amdgcn_sched_barrier(0);   // the next step's loads go before this one's sums
+            fetch(k + 64 < k1 ? k + 64 : k);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) zv[u][t] = hand_on<T>(zv[u][t]);
-#pragma unroll
-                for (int t = 0; t < R; ++t) mv[u][t] = hand_on<T>(mv[u][t]);
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
                     for (int b = 0; b < R; ++b) sum[a][b] = mma(mv[u][b], zv[u][a], sum[a][b]);
-            }
         }
         // wavefronts 2 and 3 to 0 and 1, then 1 to 0
 #pragma unroll
@@ -924,13 +936,16 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool few(int64_t s) { return s <= 256; }
 int slots_for(int64_t s, int64_t r) { return few(s) ? 16 : s <= 1024 ? 4 : r > 32 ? 2 : 1; }
 
-// Parts that dot splits len into: enough blocks for the chip, while each
-// wavefront keeps at least four steps of 64.
+// Parts that dot splits len into: with many tokens about one block a CU (4096
+// x 36864, rank 64: 69 us at 256 blocks, 78 at 512, 87 at 1024), with few two
+// for each token, in case each has an adapter of its own; each wavefront keeps
+// at least two steps of 64.
 int dot_splits(int64_t s, int64_t len, int64_t r) {
-    const int64_t tok = few(s) ? 16 : r > 64 ? 32 : 64;
-    const int64_t want = up(2 * kCus, up(s > 0 ? s : 1, tok)), most = len / 64 / 16;
-    const int64_t n = want < most ? want : most;
-    return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);
+    const int64_t most = len / 64 / 8;
+    int64_t n = few(s) ? up(2 * kCus, s > 0 ? s : 1) : up(kCus, up(s, r > 64 ? 32 : 64));
+    if (few(s)) n = n < 4 ? 4 : n > 16 ? 16 : n;
+    n = n < most ? n : most;
+    return static_cast<int>(n < 1 ? 1 : n);
 }
 
 template <typename T>
