@@ -787,46 +787,48 @@ __global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const flo
     }
 }
 
-// out_g[k, j] = sum over the chunk's tokens of f P[i, k] Z[i, j]: a block
-// takes one chunk and 128 columns of one side; of its wavefronts, WK share the
-// chunk's tiles and the others take further RT tiles of 16 ranks over the same
-// rows. Z's rows are read 16 bytes a lane (eight
-// columns of one token) and turned in registers; the ranks are the rows of
-// the matrix instruction, so a lane ends with eight neighbouring columns of
-// four ranks. The next tile's rows, and the tokens of the one after, are on
-// their way while this one's sums are formed. Tokens past the end have factors
-// of 0 and rows of 0.
-template <typename T, int RT, int WK>
-__global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
-    constexpr int WR = kWaves / WK;
-    __shared__ v4f join[WK / 2][WR][RT * 8][64];
-    const int xblocks = (x.len + 127) / 128, yblocks = (y.len + 127) / 128;
-    const int cb = blockIdx.x % (xblocks + yblocks), chunk = blockIdx.x / (xblocks + yblocks);
-    const Chunk c = plan.chunks[chunk];
-    if (c.g < 0) return;
-    const bool second = cb >= xblocks;
-    const int len = second ? y.len : x.len;
-    const int64_t ldz = second ? y.ldz : x.ldz;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    const int col = (second ? cb - xblocks : cb) * 128 + n * 8;
-    const int wk = wave % WK, wr = wave / WK, tiles = plan.rank_tiles, rt0 = (blockIdx.y * WR + wr) * RT;
-    const T* Z = static_cast<const T*>(second ? y.Z : x.Z) + (col < len ? col : 0);
-    const T* laid = static_cast<const T*>(second ? y.laid : x.laid) + lane * 8;
-    const int32_t* order = plan.order + c.first + q * 8;
-    v4f sum[RT][8];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = (c.count + 31) / 32;
+// out_g[k, j] = sum over the chunk's tokens of f P[i, k] Z[i, j]: what the two
+// kernels below share. A block takes one chunk and 128 columns of one side.
+// Z's rows are read 16 bytes a lane (eight columns of one token) and turned in
+// registers; the ranks are the rows of the matrix instruction, so a lane ends
+// with eight neighbouring columns of four ranks. Tokens past the end have
+// factors of 0 and rows of 0.
+template <typename T>
+struct GradBlock {
     typedef int v8i __attribute__((ext_vector_type(8)));
+    Chunk c;
+    const T* Z;
+    const T* laid;
+    const int32_t* order;
+    float* out;
+    int64_t ldz;
+    int len, col, chunk, steps;
+    bool second;
+
+    __device__ __forceinline__ GradBlock(const Side& x, const Side& y, int r, const Plan& plan) {
+        const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+        const int xblocks = (x.len + 127) / 128, blocks = xblocks + (y.len + 127) / 128;
+        const int cb = blockIdx.x % blocks;
+        chunk = blockIdx.x / blocks;
+        c = plan.chunks[chunk];
+        second = cb >= xblocks;
+        len = second ? y.len : x.len;
+        ldz = second ? y.ldz : x.ldz;
+        col = (second ? cb - xblocks : cb) * 128 + n * 8;
+        Z = static_cast<const T*>(second ? y.Z : x.Z) + (col < len ? col : 0);
+        laid = static_cast<const T*>(second ? y.laid : x.laid) + lane * 8;
+        order = plan.order + c.first + q * 8;
+        out = c.part < 0 ? (second ? y.out : x.out) + static_cast<int64_t>(c.g) * r * len
+                         : (second ? y.part : x.part) + static_cast<int64_t>(c.part) * r * len;
+        steps = (c.count + 31) / 32;
+    }
     // the lane's eight tokens of a tile: those past the end are not used
-    const auto tokens_of = [&](int st) {
+    __device__ __forceinline__ v8i tokens_of(int st) const {
         v8i t;
         __builtin_memcpy(&t, order + (st < steps ? st : steps - 1) * 32, sizeof(t));
         return t;
-    };
-    const auto rows_of = [&](int st, const v8i& t, Vec<T>(&rows)[8]) {
+    }
+    __device__ __forceinline__ void rows_of(int st, const v8i& t, Vec<T>(&rows)[8]) const {
         if (st * 32 + 32 <= c.count) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) rows[e] = load16(Z + static_cast<int64_t>(t[e]) * ldz);
@@ -834,28 +836,63 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 rows[e] = Vec<T>{};
-                if (st * 32 + q * 8 + e < c.count) rows[e] = load16(Z + static_cast<int64_t>(t[e]) * ldz);
+                if (st * 32 + static_cast<int>(threadIdx.x >> 4 & 3) * 8 + e < c.count)
+                    rows[e] = load16(Z + static_cast<int64_t>(t[e]) * ldz);
             }
         }
-    };
+    }
+    // the parts of a tile's factors for 16 ranks
+    __device__ __forceinline__ void factors_of(const Plan& plan, int st, int rt, Vec<T>(&f)[kParts<T>]) const {
+        const T* at = laid + (static_cast<int64_t>(c.tile + st) * plan.rank_tiles + rt) * kParts<T> * 512;
+#pragma unroll
+        for (int p = 0; p < kParts<T>; ++p) f[p] = load16(at + p * 512);
+    }
+    __device__ __forceinline__ void store(const Plan& plan, int rt, int r, const v4f(&sum)[8]) const {
+        if (col >= len) return;
+        const int ex = scale_exponent<T>(most_of(plan, second, chunk, rt));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = rt * 16 + static_cast<int>(threadIdx.x >> 4 & 3) * 4 + e;
+            if (k >= r) continue;
+            v4f lo, hi;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = ldexpf(sum[j][e], -ex);
+                hi[j] = ldexpf(sum[j + 4][e], -ex);
+            }
+            v4f* p = reinterpret_cast<v4f*>(out + static_cast<int64_t>(k) * len + col);
+            p[0] = lo;
+            p[1] = hi;
+        }
+    }
+};
+
+// Up to 32 ranks (RT tiles): every wavefront takes all ranks and every fourth
+// tile, with the next one's rows, and the tokens of the one after, on their
+// way while this one's sums are formed; the four sums are joined in LDS.
+template <typename T, int RT>
+__global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
+    __shared__ v4f join[2][RT * 8][64];
+    const GradBlock<T> b(x, y, r, plan);
+    if (b.c.g < 0) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    v4f sum[RT][8];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     Vec<T> rows[8];
-    v8i ahead = tokens_of(wk);
-    if (wk < steps) rows_of(wk, ahead, rows);
-    ahead = tokens_of(wk + WK);
-    for (int st = wk; st < steps; st += WK) {
+    auto ahead = b.tokens_of(wave);
+    if (wave < b.steps) b.rows_of(wave, ahead, rows);
+    ahead = b.tokens_of(wave + kWaves);
+    for (int st = wave; st < b.steps; st += kWaves) {
         Vec<T> f[RT][kParts<T>], columns[8];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int p = 0; p < kParts<T>; ++p) {
-                f[t][p] = Vec<T>{};
-                if (rt0 + t < tiles)
-                    f[t][p] = load16(laid + ((static_cast<int64_t>(c.tile + st) * tiles + rt0 + t) * kParts<T> + p) * 512);
-            }
+        for (int t = 0; t < RT; ++t) b.factors_of(plan, st, t, f[t]);
         transpose8<T>(rows, columns);
         __builtin_amdgcn_sched_barrier(0);
-        if (st + WK < steps) rows_of(st + WK, ahead, rows);
-        ahead = tokens_of(st + 2 * WK);
+        if (st + kWaves < b.steps) b.rows_of(st + kWaves, ahead, rows);
+        ahead = b.tokens_of(st + 2 * kWaves);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int p = 0; p < kParts<T>; ++p)
@@ -865,44 +902,80 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
                 for (int j = 0; j < 8; ++j) sum[t][j] = mma(f[t][p], columns[j], sum[t][j]);
     }
 #pragma unroll
-    for (int half = WK / 2; half >= 1; half /= 2) {
+    for (int half = 2; half >= 1; half /= 2) {
         __syncthreads();
-        if (wk >= half && wk < 2 * half) {
+        if (wave >= half && wave < 2 * half) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) join[wk - half][wr][t * 8 + j][lane] = sum[t][j];
+                for (int j = 0; j < 8; ++j) join[wave - half][t * 8 + j][lane] = sum[t][j];
         }
         __syncthreads();
-        if (wk < half) {
+        if (wave < half) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[t][j] += join[wk][wr][t * 8 + j][lane];
+                for (int j = 0; j < 8; ++j) sum[t][j] += join[wave][t * 8 + j][lane];
         }
     }
-    if (wk != 0 || col >= len) return;
-    float* out = c.part < 0 ? (second ? y.out : x.out) + static_cast<int64_t>(c.g) * r * len
-                            : (second ? y.part : x.part) + static_cast<int64_t>(c.part) * r * len;
+    if (wave != 0) return;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        if (rt0 + t >= tiles) continue;
-        const int ex = scale_exponent<T>(most_of(plan, second, chunk, rt0 + t));
+    for (int t = 0; t < RT; ++t) b.store(plan, t, r, sum[t]);
+}
+
+// More ranks: the wavefronts divide the ranks (RW tiles of 16 each). Each
+// reads and turns one tile of a round of four and leaves it in LDS for all, so
+// that Z is read once and every wavefront has rows of its own on their way.
+template <typename T, int RW>
+__global__ __launch_bounds__(kThreads, 2) void k_lora_grad_shared(Side x, Side y, int r, Plan plan) {
+    __shared__ Vec<T> turned[kWaves][8][64];
+    const GradBlock<T> b(x, y, r, plan);
+    if (b.c.g < 0) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    v4f sum[RW][8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int k = (rt0 + t) * 16 + q * 4 + e;
-            if (k >= r) continue;
-            v4f lo, hi;
+    for (int t = 0; t < RW; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[j] = ldexpf(sum[t][j][e], -ex);
-                hi[j] = ldexpf(sum[t][j + 4][e], -ex);
+        for (int j = 0; j < 8; ++j) sum[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    Vec<T> rows[8];
+    auto ahead = b.tokens_of(wave);
+    if (wave < b.steps) b.rows_of(wave, ahead, rows);
+    ahead = b.tokens_of(wave + kWaves);
+    for (int st0 = 0; st0 < b.steps; st0 += kWaves) {
+        const int st = st0 + wave;
+        Vec<T> f[kWaves][RW][kParts<T>], columns[8];
+#pragma unroll
+        for (int u = 0; u < kWaves; ++u)
+#pragma unroll
+            for (int t = 0; t < RW; ++t) {
+                const int rt = wave * RW + t;
+                b.factors_of(plan, st0 + u < b.steps ? st0 + u : b.steps - 1,
+                             rt < plan.rank_tiles ? rt : plan.rank_tiles - 1, f[u][t]);
             }
-            v4f* p = reinterpret_cast<v4f*>(out + static_cast<int64_t>(k) * len + col);
-            p[0] = lo;
-            p[1] = hi;
+        transpose8<T>(rows, columns);
+        // LDS alone is waited for: the factors stay on their way
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the last round's reads have ended
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turned[wave][j][lane] = columns[j];
+        if (st + kWaves < b.steps) b.rows_of(st + kWaves, ahead, rows);
+        ahead = b.tokens_of(st + 2 * kWaves);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < kWaves; ++u) {
+            if (st0 + u >= b.steps) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const Vec<T> z = turned[u][j][lane];
+#pragma unroll
+                for (int t = 0; t < RW; ++t)
+#pragma unroll
+                    for (int p = 0; p < kParts<T>; ++p) sum[t][j] = mma(f[u][t][p], z, sum[t][j]);
+            }
         }
     }
+#pragma unroll
+    for (int t = 0; t < RW; ++t)
+        if (wave * RW + t < plan.rank_tiles) b.store(plan, wave * RW + t, r, sum[t]);
 }
 
 // Adapters of several chunks: their partial sums in order. Adapters that no
@@ -1056,7 +1129,7 @@ struct Layout {
 
     Layout(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) : d(w, s, o, r) {
         // chunks as long as still leave about 1024 blocks
-        const int64_t blocks = (up(h, 128) + up(o, 128)) * up(r, 64);
+        const int64_t blocks = up(h, 128) + up(o, 128);
         const int64_t kc = up(up(s > 0 ? s : 1, up(4 * kCus, blocks)), 128) * 128;
         KC = static_cast<int>(kc);
         const int64_t groups = G < s ? G : s, rt = up(r, 16);
@@ -1085,10 +1158,10 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     char* ws = static_cast<char*>(workspace);
     const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    const unsigned rt = static_cast<unsigned>(up(a.r, 16)), slots = static_cast<unsigned>(l.slots);
+    const int rt = static_cast<int>(up(a.r, 16));
     const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
                     reinterpret_cast<Chunk*>(ws + l.chunks), reinterpret_cast<uint32_t*>(ws + l.most), l.slots,
-                    l.tiles, static_cast<int>(rt)};
+                    l.tiles, rt};
     float* dT = floats(l.dT);
     const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
     const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
@@ -1109,17 +1182,11 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
             k_lora_most<<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         k_lora_lay<T><<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        const auto go = [&](auto n, auto wk) {
-            constexpr int RT = decltype(n)::value, WK = decltype(wk)::value;
-            const unsigned blocks = static_cast<unsigned>(up(a.h, 128) + up(a.o, 128));
-            k_lora_grad<T, RT, WK>
-                <<<dim3(slots * blocks, static_cast<unsigned>(up(rt, RT * (kWaves / WK)))), kThreads, 0, stream>>>(
-                    x, y, r, plan);
-        };
-        using std::integral_constant;
-        if (rt == 1) go(integral_constant<int, 1>(), integral_constant<int, 4>());
-        else if (rt == 2) go(integral_constant<int, 2>(), integral_constant<int, 4>());
-        else go(integral_constant<int, 2>(), integral_constant<int, 2>());
+        const unsigned blocks = static_cast<unsigned>(l.slots * (up(a.h, 128) + up(a.o, 128)));
+        if (rt == 1) k_lora_grad<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+        else if (rt == 2) k_lora_grad<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+        else if (rt <= 4) k_lora_grad_shared<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+        else k_lora_grad_shared<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t fours = static_cast<int64_t>(r) * (a.h + a.o) / 4;
