@@ -410,6 +410,10 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
         }
     }
     __syncthreads();
+    const float f = g < 0 ? 0.0f : scale[g];
+    float factor[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) factor[e] = factor_of(f, exps[q * 4 + e]);
     if (inside && out != base) {         // rows without an adapter are base's
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -426,10 +430,6 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[j], sum[j]);
     }
-    const float f = scale[g];
-    float factor[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) factor[e] = factor_of(f, exps[q * 4 + e]);
     if (inside) store_sums<T>(out, first, ldo, col, q, tokens, b, sum, factor);
 }
 
@@ -603,7 +603,7 @@ struct Plan {
     int32_t* part;                   // [G]: its first partial sums
     int32_t* tile_chunk;             // [tiles]: the chunk of each tile, or -1
     Chunk* chunks;                   // [slots]
-    uint32_t* most;                  // [2][slots][rank tiles]: largest |factor|, as fp32 bits
+    float* most;                     // [2 rank tiles][tiles]: the largest |factor|
     int slots, tiles, rank_tiles;
 };
 
@@ -671,8 +671,6 @@ __global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __res
                           used > 1 ? part + c : -1};
             plan.chunks[k] = e;
         }
-        for (int k = begin * plan.rank_tiles + threadIdx.x; k < end * plan.rank_tiles; k += kPlanThreads)
-            plan.most[k] = plan.most[plan.slots * plan.rank_tiles + k] = 0;
         const int tile_end = last ? plan.tiles : (C + n + 31) / 32 + D + 1;
         for (int k = tile0 + threadIdx.x; k < tile_end; k += kPlanThreads)
             plan.tile_chunk[k] = (k - tile0) * 32 < n ? begin + (k - tile0) * 32 / KC : -1;
@@ -731,31 +729,32 @@ struct TileFactors {
     }
 };
 
-// The largest |f_g P| of each chunk and rank tile, for both sides: a block
-// takes one tile, a wavefront one rank tile of one side at a time. The maximum
-// of the bits of non-negative numbers is that of the numbers, in any order.
-// NaN counts as infinity.
+// The largest |f_g P| of each tile and 16 ranks, for both sides: a block takes
+// one tile, a wavefront one task (16 ranks of one side). NaN counts as
+// infinity.
 __global__ __launch_bounds__(kThreads) void k_lora_most(Side x, Side y, const float* __restrict__ scale, int r,
                                                         Plan plan) {
-    const int chunk = plan.tile_chunk[blockIdx.x];
-    if (chunk < 0) return;
+    const int chunk = plan.tile_chunk[blockIdx.x], tasks = 2 * plan.rank_tiles;
+    const int task = blockIdx.y * kWaves + (threadIdx.x >> 6);
+    if (chunk < 0 || task >= tasks) return;
     const TileFactors t(plan, plan.chunks[chunk], scale, r);
-    const int lane = threadIdx.x & 63;
-    for (int task = threadIdx.x >> 6; task < 2 * plan.rank_tiles; task += kWaves) {
-        const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
-        float v[8], most = 0.0f;
-        t.load(which ? y.P : x.P, rt * 16 + (lane & 15), r, v);
+    const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
+    float v[8], most = 0.0f;
+    t.load(which ? y.P : x.P, rt * 16 + (threadIdx.x & 15), r, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, v[e] == v[e] ? fabsf(v[e]) : __builtin_inff());
-        most = wave_max(most);
-        if (lane == 0)
-            atomicMax(plan.most + (which * plan.slots + chunk) * plan.rank_tiles + rt,
-                      __builtin_bit_cast(uint32_t, most));
-    }
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, v[e] == v[e] ? fabsf(v[e]) : __builtin_inff());
+    most = wave_max(most);
+    if ((threadIdx.x & 63) == 0) plan.most[static_cast<int64_t>(task) * plan.tiles + blockIdx.x] = most;
 }
 
-__device__ __forceinline__ float most_of(const Plan& plan, int side, int chunk, int rt) {
-    return __builtin_bit_cast(float, plan.most[(side * plan.slots + chunk) * plan.rank_tiles + rt]);
+// The power of two of a chunk and task, from all its tiles.
+template <typename T>
+__device__ __forceinline__ int exponent_of(const Plan& plan, const Chunk& c, int task) {
+    if constexpr (!kScaled<T>) return 0;
+    const float* at = plan.most + static_cast<int64_t>(task) * plan.tiles + c.tile;
+    float most = 0.0f;
+    for (int st = threadIdx.x & 63; st < (c.count + 31) / 32; st += 64) most = fmaxf(most, at[st]);
+    return scale_exponent<T>(wave_max(most));
 }
 
 // Lays f_g P out as the matrix instruction takes it: a block takes one tile, a
@@ -764,12 +763,14 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const float* __restrict__ scale, int r,
                                                        Plan plan) {
     const int chunk = plan.tile_chunk[blockIdx.x];
-    if (chunk < 0) return;
-    const TileFactors t(plan, plan.chunks[chunk], scale, r);
+    const int task = blockIdx.y * kWaves + (threadIdx.x >> 6);
+    if (chunk < 0 || task >= 2 * plan.rank_tiles) return;
+    const Chunk c = plan.chunks[chunk];
+    const TileFactors t(plan, c, scale, r);
     const int lane = threadIdx.x & 63, n = lane & 15;
-    for (int task = threadIdx.x >> 6; task < 2 * plan.rank_tiles; task += kWaves) {
+    {
         const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
-        const int ex = scale_exponent<T>(most_of(plan, which, chunk, rt));
+        const int ex = exponent_of<T>(plan, c, task);
         float v[8];
         t.load(which ? y.P : x.P, rt * 16 + n, r, v);
         Vec<T> out[kParts<T>];
@@ -808,7 +809,7 @@ struct GradBlock {
     __device__ __forceinline__ GradBlock(const Side& x, const Side& y, int r, const Plan& plan) {
         const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
         const int xblocks = (x.len + 127) / 128, blocks = xblocks + (y.len + 127) / 128;
-        const int cb = blockIdx.x % blocks;
+        const int cb = blocks - 1 - static_cast<int>(blockIdx.x % blocks);
         chunk = blockIdx.x / blocks;
         c = plan.chunks[chunk];
         second = cb >= xblocks;
@@ -848,12 +849,11 @@ struct GradBlock {
         for (int p = 0; p < kParts<T>; ++p) f[p] = load16(at + p * 512);
     }
     __device__ __forceinline__ void store(const Plan& plan, int rt, int r, const v4f(&sum)[8]) const {
-        if (col >= len) return;
-        const int ex = scale_exponent<T>(most_of(plan, second, chunk, rt));
+        const int ex = exponent_of<T>(plan, c, second * plan.rank_tiles + rt);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int k = rt * 16 + static_cast<int>(threadIdx.x >> 4 & 3) * 4 + e;
-            if (k >= r) continue;
+            if (k >= r || col >= len) continue;
             v4f lo, hi;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1005,14 +1005,15 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // each adapter of a tile. With many, most tiles have one: where a pass does
 // not take two of them, the second has a block of its own, which leaves at
 // once in all other tiles (4096 x 36864, rank 64, two adapters that meet
-// inside a tile: 145 us for the one block's two passes, 95 for two blocks).
+// inside a tile: 145 us for the one block's two passes, 107 for two blocks).
 bool few(int64_t s) { return s <= 256; }
 int slots_for(int64_t s, int64_t r) { return few(s) ? 16 : s <= 1024 ? 4 : r > 32 ? 2 : 1; }
 
-// Parts that dot splits len into: with many tokens about one block a CU (4096
-// x 36864, rank 64: 69 us at 256 blocks, 78 at 512, 87 at 1024), with few two
-// for each token, in case each has an adapter of its own; each wavefront keeps
-// at least two steps of 64.
+// Parts that dot splits len into; each wavefront keeps at least two steps of
+// 64. Few tokens: two blocks for each, in case each has an adapter of its own.
+// Many: about one block a CU (4096 x 36864, rank 64: 69 us at 256 blocks, 78
+// at 512, 87 at 1024; where tiles with two adapters add a few blocks, 107 at
+// 256 and 112 at 448).
 int dot_splits(int64_t s, int64_t len, int64_t r) {
     const int64_t most = len / 64 / 8;
     int64_t n = few(s) ? up(2 * kCus, s > 0 ? s : 1) : up(kCus, up(s, r > 64 ? 32 : 64));
@@ -1128,9 +1129,10 @@ struct Layout {
     DotPlaces d;
 
     Layout(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) : d(w, s, o, r) {
-        // chunks as long as still leave about 1024 blocks
+        // chunks as long as still leave about 1024 blocks, up to 1024 tiles
         const int64_t blocks = up(h, 128) + up(o, 128);
-        const int64_t kc = up(up(s > 0 ? s : 1, up(4 * kCus, blocks)), 128) * 128;
+        int64_t kc = up(up(s > 0 ? s : 1, up(4 * kCus, blocks)), 128) * 128;
+        kc = kc < 32768 ? kc : 32768;
         KC = static_cast<int>(kc);
         const int64_t groups = G < s ? G : s, rt = up(r, 16);
         slots = static_cast<int>(s / kc + groups + 1);
@@ -1142,7 +1144,7 @@ struct Layout {
         part = w.take(4 * G);
         tile_chunk = w.take(4 * tiles);
         chunks = w.take(static_cast<int64_t>(sizeof(Chunk)) * slots);
-        most = w.take(4 * 2 * slots * rt);
+        most = w.take(4 * 2 * rt * tiles);
         for (int k = 0; k < 2; ++k) {
             laid[k] = w.take(tiles * rt * 3 * 512 * 2);
             sums[k] = w.take(4 * parts * r * (k == 0 ? h : o));
@@ -1160,7 +1162,7 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const int rt = static_cast<int>(up(a.r, 16));
     const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
-                    reinterpret_cast<Chunk*>(ws + l.chunks), reinterpret_cast<uint32_t*>(ws + l.most), l.slots,
+                    reinterpret_cast<Chunk*>(ws + l.chunks), floats(l.most), l.slots,
                     l.tiles, rt};
     float* dT = floats(l.dT);
     const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
@@ -1175,12 +1177,10 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
         if ((e = dot<T>(a, dY, lddy, a.B, a.o, P, stream)) != hipSuccess) return e;
         if ((e = join<T>(a, dot_splits(a.s, a.o, r), P, dT, ws + l.d.parts, ints(l.d.exps), stream)) != hipSuccess)
             return e;
-        if (dX && (e = add_many<T>(a, ws + l.d.parts, ints(l.d.exps), a.A, a.h, base, ldb, dX, lddx, stream)) !=
-                      hipSuccess)
-            return e;
+        const dim3 per_tile(static_cast<unsigned>(l.tiles), static_cast<unsigned>(up(2 * rt, kWaves)));
         if constexpr (kScaled<T>)
-            k_lora_most<<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
-        k_lora_lay<T><<<static_cast<unsigned>(l.tiles), kThreads, 0, stream>>>(x, y, a.scale, r, plan);
+            k_lora_most<<<per_tile, kThreads, 0, stream>>>(x, y, a.scale, r, plan);
+        k_lora_lay<T><<<per_tile, kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const unsigned blocks = static_cast<unsigned>(l.slots * (up(a.h, 128) + up(a.o, 128)));
         if (rt == 1) k_lora_grad<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
@@ -1188,6 +1188,9 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
         else if (rt <= 4) k_lora_grad_shared<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
         else k_lora_grad_shared<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (dX && (e = add_many<T>(a, ws + l.d.parts, ints(l.d.exps), a.A, a.h, base, ldb, dX, lddx, stream)) !=
+                      hipSuccess)
+            return e;
     }
     const int64_t fours = static_cast<int64_t>(r) * (a.h + a.o) / 4;
     k_lora_grad_sum<<<dim3(static_cast<unsigned>(up(fours, kThreads)), static_cast<unsigned>(a.G)), kThreads, 0,
