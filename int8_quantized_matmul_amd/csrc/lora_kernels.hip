@@ -288,19 +288,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
 // bytes of a token at a time.
 constexpr int kAddColumns = kWaves * 128;
 
-// Eight operands of 16 ranks (both parts alike) x 16 columns of M's rows
-// [st 16, st 16 + 16): operand j holds column mcol + j of each lane. Ranks
-// past r are 0.
+// M's rows [st 16, st 16 + 16) for eight operands of 16 ranks (both parts
+// alike) x 16 columns; turned, operand j holds column mcol + j of each lane.
+// Ranks past r are 0.
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* Mg, int64_t len, int r, int st, int q, int mcol, Vec<T>(&rows)[8]) {
+    const int k0 = st * 16 + (q & 1) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) rows[k] = load16(Mg + (k0 + k < r ? k0 + k : r - 1) * len + mcol);
+    if (st * 16 + 16 > r) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k >= r) rows[k] = Vec<T>{};
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void load_ranks(const T* Mg, int64_t len, int r, int st, int q, int mcol,
                                            Vec<T>(&columns)[8]) {
-    const int k0 = st * 16 + (q & 1) * 8;
     Vec<T> rows[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        rows[k] = Vec<T>{};
-        if (k0 + k < r) rows[k] = load16(Mg + (k0 + k) * len + mcol);
-    }
+    load_rows<T>(Mg, len, r, st, q, mcol, rows);
     transpose8<T>(rows, columns);
 }
 
@@ -329,6 +336,22 @@ __device__ __forceinline__ void store_sums(T* out, int64_t first, int64_t ldo, i
     }
 }
 
+// The sum of a value's splits, `stride` apart, in their order. Eight loads are
+// on their way at once: one after another they cost a trip to L2 each (64
+// decoded tokens, 8 splits: add took 28 us instead of %FEW%).
+__device__ __forceinline__ float join_splits(const float* p, int64_t stride, int splits) {
+    float v = 0.0f;
+    for (int u0 = 0; u0 < splits; u0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = p[(u0 + e < splits ? u0 + e : splits - 1) * stride];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (u0 + e < splits) v += x[e];
+    }
+    return v;
+}
+
 // Few tokens: a block takes 16 tokens, 512 columns and one of the tile's
 // adapters (slots = 16, so each has its own; a block without one leaves). It
 // joins the splits of its tokens' P itself, while M's first ranks and base are
@@ -342,6 +365,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
                                                               float* __restrict__ Tout) {
     constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
     __shared__ __align__(16) T parts[16 * kSteps * 32];
+    __shared__ float values[16][kSteps * 16 + 1];
     __shared__ int exps[16];
     const int steps = (r + 15) / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
@@ -367,8 +391,8 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
     const bool inside = col < len;
     const int mcol = inside ? col : 0;
     const T* Mg = M + (g < 0 ? 0 : g) * r * len;
-    Vec<T> columns[8], b[4];
-    if (g >= 0) load_ranks<T>(Mg, len, r, 0, q, mcol, columns);
+    Vec<T> rows[8], b[4];                // on their way until the parts are laid out
+    if (g >= 0) load_rows<T>(Mg, len, r, 0, q, mcol, rows);
     const uint64_t touched = (tokens | (slot == 0 ? none : 0)) & (s - first < 16 ? (1ull << (s - first)) - 1 : 0xffff);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -379,30 +403,25 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
         const int t = threadIdx.x / 16, sub = threadIdx.x % 16;
         const int64_t it = first + t;
         const bool mine = touched >> t & 1;
-        float v[kSteps], most = 0.0f;
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            v[st] = 0.0f;
-            if (st >= steps) continue;
+        float most = 0.0f;
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st) {
             const int k = st * 16 + sub;
-            if (mine && k < r) {
-                const float* p = P + it * r + k;
-#pragma unroll 4
-                for (int u = 0; u < splits; ++u) v[st] += p[static_cast<int64_t>(u) * s * r];
-                if (Tout && cb == 0) Tout[it * r + k] = v[st];
-            }
+            const bool real = mine && k < r;
+            const float sum = join_splits(P + (real ? it * r + k : 0), s * r, splits);
+            if (real && Tout && cb == 0) Tout[it * r + k] = sum;
+            values[t][k] = real ? sum : 0.0f;
             // NaN counts as infinity: no power of two for the row
-            most = fmaxf(most, v[st] == v[st] ? fabsf(v[st]) : __builtin_inff());
+            if (real) most = fmaxf(most, sum == sum ? fabsf(sum) : __builtin_inff());
         }
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
         const int ex = scale_exponent<T>(most);
         if (sub == 0) exps[t] = ex;
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            if (st >= steps) continue;
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st) {
             T part[2];
-            split<T, 2>(v[st], ex, part);
+            split<T, 2>(values[t][st * 16 + sub], ex, part);      // the lane's own
             // [step][eight ranks][token]: the lanes of the matrix instruction in order
             T* to = parts + ((st * 4 + sub / 8) * 16 + t) * 8 + sub % 8;
             to[0] = part[0];
@@ -425,7 +444,9 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int st = 0; st < steps; ++st) {
-        if (st > 0) load_ranks<T>(Mg, len, r, st, q, mcol, columns);
+        Vec<T> columns[8];
+        if (st > 0) load_rows<T>(Mg, len, r, st, q, mcol, rows);
+        transpose8<T>(rows, columns);
         const Vec<T> p = load16(parts + (st * 64 + lane) * 8);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[j], sum[j]);
@@ -447,12 +468,13 @@ __global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict_
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
         v[st] = 0.0f;
+        if (st >= steps) continue;
         const int k = st * 16 + sub;
-        if (i < s && k < r) {
-            const float* p = P + i * r + k;
-#pragma unroll 4
-            for (int u = 0; u < splits; ++u) v[st] += p[static_cast<int64_t>(u) * s * r];
-            if (Tout) Tout[i * r + k] = v[st];
+        const bool real = i < s && k < r;
+        const float sum = join_splits(P + (real ? i * r + k : 0), s * r, splits);
+        if (real) {
+            v[st] = sum;
+            if (Tout) Tout[i * r + k] = sum;
         }
         most = fmaxf(most, v[st] == v[st] ? fabsf(v[st]) : __builtin_inff());
     }
@@ -720,12 +742,15 @@ struct TileFactors {
         const int p0 = (static_cast<int>(blockIdx.x) - c.tile) * 32 + (threadIdx.x >> 4 & 3) * 8;
         f = scale[c.g];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            at[e] = p0 + e < c.count ? static_cast<int64_t>(plan.order[c.first + p0 + e]) * r : -1;
+        for (int e = 0; e < 8; ++e) at[e] = plan.order[c.first + p0 + e];   // 32 more than there are tokens
+#pragma unroll
+        for (int e = 0; e < 8; ++e) at[e] = p0 + e < c.count ? at[e] * r : -1;
     }
     __device__ __forceinline__ void load(const float* P, int k, int r, float(&v)[8]) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = at[e] >= 0 && k < r ? f * P[at[e] + k] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = P[(at[e] < 0 ? 0 : at[e]) + (k < r ? k : r - 1)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = at[e] >= 0 && k < r ? f * v[e] : 0.0f;
     }
 };
 
