@@ -109,6 +109,40 @@ __device__ __forceinline__ void split(float v, int ex, T(&part)[N]) {
     }
 }
 
+// Few tokens (at most kFew): a block takes one adapter and finds its tokens
+// itself. `slots` = min(G, s) blocks stand for the adapters: adapter `slot` if
+// there are no more adapters than tokens, else that of token `slot`, unless an
+// earlier token has it too. One slot more stands for the tokens without one.
+// tokens: their list; count: how many, 0 for a block without work.
+constexpr int kFew = 256;
+
+struct FewTokens {
+    int64_t g;                       // the adapter, or -1 for tokens without one
+    int count;
+
+    __device__ __forceinline__ FewTokens(const int32_t* ids, int s, int64_t G, int slot, int slots,
+                                         int (&tokens)[kFew], int (&counts)[kWaves]) {
+        const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+        int id = i < s ? ids[i] : -2;
+        if (i < s && (id < 0 || id >= G)) id = -1;
+        g = slot == slots ? -1 : G <= s ? slot : ids[slot];
+        if (g < 0 || g >= G) g = -1;
+        const uint64_t vote = __ballot(id == g);
+        if (lane == 0) counts[wave] = __popcll(vote);
+        __syncthreads();
+        int at = 0;
+        count = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) at += counts[w];
+            count += counts[w];
+        }
+        if (id == g) tokens[at + __popcll(vote & ((1ull << lane) - 1))] = i;
+        __syncthreads();
+        if (slot < slots && (g < 0 || (count > 0 && G > s && tokens[0] != slot))) count = 0;
+    }
+};
+
 // The distinct adapters among the tokens of a tile, in the order of their
 // first tokens; every lane of every wavefront walks them alike. id: the id of
 // the tile's token lane % TOK, or -1 for none.
@@ -143,7 +177,10 @@ struct Adapters {
 // rows past the end are read from the last row and their sums dropped. Of the
 // tile's adapters the block takes every `slots`-th, and up to NA of them in
 // one pass over Z: a tile where one request ends and the next begins costs no
-// second pass.
+// second pass. Bound by memory up to 32 ranks (4096 x 12288, rank 16: 24-30 us,
+// 3.4-4.2 TB/s, 20 for one adapter) and by the CU's loads beyond, where M's
+// pieces are as many as Z's (4096 x 36864, rank 64: 69 us for one adapter, 4.4
+// TB/s). The next step's loads go before this one's sums (78 us without).
 template <typename T, int MT, int RT, int NA>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ Z, int64_t ldz,
                                                           const T* __restrict__ M, int64_t G, int r, int len,
@@ -153,10 +190,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     __shared__ v4f join[2][MT * RT * NA][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     // Neighbouring blocks go to different XCDs, so a slot's blocks are neighbours:
-    // most of the higher slots' have nothing to do. With many tokens those few
-    // start first, since they end last.
+    // most of the higher slots' have nothing to do. Those that do start first,
+    // since they end last.
     const int tile = blockIdx.x % tiles, part = blockIdx.x / tiles % splits;
-    const int turn0 = blockIdx.x / tiles / splits, slot = MT == 1 ? turn0 : slots - 1 - turn0;
+    const int slot = slots - 1 - blockIdx.x / tiles / splits;
     const int64_t first = static_cast<int64_t>(tile) * TOK;
     const int steps = len / 64, w = part * kWaves + wave, all = splits * kWaves;
     const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w / all) * 64;
@@ -276,6 +313,93 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     if (NA == 2 && held == 1) pass(std::integral_constant<int, 1>(), g, tokens);
 }
 
+// dot for few tokens: a block takes one adapter's tokens, 16 at a time, every
+// `spread`-th 16 of them, and one of `splits` parts of len; its wavefronts each
+// a quarter of that. M, which is what has to be read, is read once for each 16.
+template <typename T, int RT>
+__global__ __launch_bounds__(kThreads, 2) void k_lora_dot_few(const T* __restrict__ Z, int64_t ldz,
+                                                              const T* __restrict__ M, int64_t G, int r, int len,
+                                                              const int32_t* __restrict__ ids, int s, int slots,
+                                                              int spread, int splits, float* __restrict__ P) {
+    __shared__ v4f join[2][RT][64];
+    __shared__ int tokens[kFew], counts[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
+    const int part = blockIdx.x % splits, group0 = blockIdx.x / splits % spread, slot = blockIdx.x / splits / spread;
+    const FewTokens mine(ids, s, G, slot, slots, tokens, counts);
+    P += static_cast<int64_t>(part) * s * r;
+    if (mine.g < 0) {                    // tokens without an adapter
+        for (int k = threadIdx.x; group0 == 0 && k < mine.count * r; k += kThreads)
+            P[static_cast<int64_t>(tokens[k / r]) * r + k % r] = 0.0f;
+        return;
+    }
+    const int steps = len / 64, w = part * kWaves + wave, all = splits * kWaves;
+    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w / all) * 64;
+    const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (w + 1) / all) * 64;
+    const int lrow = lane >> 2, lpiece = (lane & 3) * 8;
+    const T* m[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int k = t * 16 + lrow;
+        m[t] = M + (mine.g * r + (k < r ? k : r - 1)) * len + lpiece;
+    }
+    for (int first = group0 * 16; first < mine.count; first += spread * 16) {
+        const int zi = tokens[first + lrow < mine.count ? first + lrow : mine.count - 1];
+        const T* z = Z + zi * ldz + lpiece;
+        v4f sum[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) sum[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        Vec<T> zn[2], mn[2][RT];         // the step on its way
+        const auto fetch = [&](int k) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                zn[u] = load16(z + k + u * 32);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) mn[u][t] = load16(m[t] + k + u * 32);
+            }
+        };
+        if (k0 < k1) fetch(k0);
+        for (int k = k0; k < k1; k += 64) {
+            Vec<T> zv[2], mv[2][RT];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                zv[u] = hand_on<T>(zn[u]);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) mv[u][t] = hand_on<T>(mn[u][t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(k + 64 < k1 ? k + 64 : k);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) sum[t] = mma(mv[u][t], zv[u], sum[t]);
+        }
+#pragma unroll
+        for (int half = 2; half >= 1; half /= 2) {
+            __syncthreads();
+            if (wave >= half && wave < 2 * half) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) join[wave - half][t][lane] = sum[t];
+            }
+            __syncthreads();
+            if (wave < half) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) sum[t] += join[wave][t][lane];
+            }
+        }
+        if (wave == 0 && first + n < mine.count) {
+            float* p = P + static_cast<int64_t>(tokens[first + n]) * r;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int k = t * 16 + q * 4 + e;
+                    if (k < r) p[k] = sum[t][e];
+                }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // add: out_i = base_i + f_g P_i M_g.
 //
@@ -337,8 +461,8 @@ __device__ __forceinline__ void store_sums(T* out, int64_t first, int64_t ldo, i
 }
 
 // The sum of a value's splits, `stride` apart, in their order. Eight loads are
-// on their way at once: one after another they cost a trip to L2 each (64
-// decoded tokens, 8 splits: add took 28 us instead of %FEW%).
+// on their way at once: one after another they cost a trip to L2 each (add for
+// 64 decoded tokens, 8 splits: 27.6 us one after another, 21.9 at once).
 __device__ __forceinline__ float join_splits(const float* p, int64_t stride, int splits) {
     float v = 0.0f;
     for (int u0 = 0; u0 < splits; u0 += 8) {
@@ -352,63 +476,62 @@ __device__ __forceinline__ float join_splits(const float* p, int64_t stride, int
     return v;
 }
 
-// Few tokens: a block takes 16 tokens, 512 columns and one of the tile's
-// adapters (slots = 16, so each has its own; a block without one leaves). It
-// joins the splits of its tokens' P itself, while M's first ranks and base are
-// on their way, and its first columns' blocks also write them to T.
+// Few tokens: a block takes one adapter's tokens, 16 at a time, every
+// `spread`-th 16 of them, and 512 columns. It joins the splits of its tokens'
+// P itself, while M's first ranks and base are on their way, and its first
+// columns' blocks also write them to T. Bound by the trips to memory that a
+// block makes one after another (ids; P, M and base; out): 64 tokens with 24
+// adapters of rank 16, 36864 columns: 16 us for 38 MB, 2.4 TB/s (18 us with a
+// block for each 16 neighbouring tokens and adapter, which reads an adapter
+// again for every 16). A second group of 512 columns a block, with its own
+// loads on their way, took 22 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __restrict__ P, int splits,
                                                               const T* __restrict__ M, int64_t G, int r, int len,
                                                               const int32_t* __restrict__ ids,
                                                               const float* __restrict__ scale, const T* base,
-                                                              int64_t ldb, T* out, int64_t ldo, int64_t s,
-                                                              float* __restrict__ Tout) {
+                                                              int64_t ldb, T* out, int64_t ldo, int s, int slots,
+                                                              int spread, float* __restrict__ Tout) {
     constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
     __shared__ __align__(16) T parts[16 * kSteps * 32];
     __shared__ float values[16][kSteps * 16 + 1];
-    __shared__ int exps[16];
+    __shared__ int exps[16], tokens[kFew], counts[kWaves];
     const int steps = (r + 15) / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     const int col_blocks = (len + kAddColumns - 1) / kAddColumns;
-    const int cb = blockIdx.x % col_blocks, slot = blockIdx.x / col_blocks % 16;
-    const int64_t first = static_cast<int64_t>(blockIdx.x / col_blocks / 16) * 16;
-    Adapters<16> adapters(ids, first, s, G);
-    const uint64_t none = ~adapters.left & 0xffff;
-    int64_t g = -1;
-    uint64_t tokens = 0;
-    for (int turn = 0; adapters.left; ++turn) {
-        uint64_t mine;
-        const int id = adapters.next(mine);
-        if (turn == slot) {
-            g = id;
-            tokens = mine;
-            break;
-        }
-    }
-    if (g < 0 && slot != 0) return;
-
+    const int cb = blockIdx.x % col_blocks, group0 = blockIdx.x / col_blocks % spread;
+    const int slot = blockIdx.x / col_blocks / spread;
+    const FewTokens mine(ids, s, G, slot, slots, tokens, counts);
     const int col = cb * kAddColumns + wave * 128 + n * 8;  // this lane's columns
     const bool inside = col < len;
     const int mcol = inside ? col : 0;
-    const T* Mg = M + (g < 0 ? 0 : g) * r * len;
-    Vec<T> rows[8], b[4];                // on their way until the parts are laid out
-    if (g >= 0) load_rows<T>(Mg, len, r, 0, q, mcol, rows);
-    const uint64_t touched = (tokens | (slot == 0 ? none : 0)) & (s - first < 16 ? (1ull << (s - first)) - 1 : 0xffff);
+    const T* Mg = M + (mine.g < 0 ? 0 : mine.g) * r * len;
+    const float f = mine.g < 0 ? 0.0f : scale[mine.g];
+    for (int first = group0 * 16; first < mine.count; first += spread * 16) {
+        Vec<T> rows[8], b[4];            // on their way until the parts are laid out
+        int at[4];                       // this lane's tokens, or -1
+        if (mine.g >= 0) load_rows<T>(Mg, len, r, 0, q, mcol, rows);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        b[e] = Vec<T>{};
-        if (base && inside && (touched >> (q * 4 + e) & 1)) b[e] = load16(piece_of(base, first, q, e, ldb, col));
-    }
-    {
+        for (int e = 0; e < 4; ++e) {
+            at[e] = inside && first + q * 4 + e < mine.count ? tokens[first + q * 4 + e] : -1;
+            b[e] = Vec<T>{};
+            if (base && at[e] >= 0) b[e] = load16(base + static_cast<int64_t>(at[e]) * ldb + col);
+        }
         const int t = threadIdx.x / 16, sub = threadIdx.x % 16;
-        const int64_t it = first + t;
-        const bool mine = touched >> t & 1;
+        const int64_t it = first + t < mine.count ? tokens[first + t] : -1;
+        if (mine.g < 0) {                // tokens without an adapter are base's
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (at[e] >= 0 && out != base) *reinterpret_cast<Vec<T>*>(out + static_cast<int64_t>(at[e]) * ldo + col) = b[e];
+            for (int k = sub; Tout && cb == 0 && it >= 0 && k < r; k += 16) Tout[it * r + k] = 0.0f;
+            continue;
+        }
         float most = 0.0f;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
             const int k = st * 16 + sub;
-            const bool real = mine && k < r;
-            const float sum = join_splits(P + (real ? it * r + k : 0), s * r, splits);
+            const bool real = it >= 0 && k < r;
+            const float sum = join_splits(P + (real ? it * r + k : 0), static_cast<int64_t>(s) * r, splits);
             if (real && Tout && cb == 0) Tout[it * r + k] = sum;
             values[t][k] = real ? sum : 0.0f;
             // NaN counts as infinity: no power of two for the row
@@ -417,6 +540,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
         const int ex = scale_exponent<T>(most);
+        __syncthreads();                 // the last 16 tokens' parts have been read
         if (sub == 0) exps[t] = ex;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
@@ -427,31 +551,27 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
             to[0] = part[0];
             to[2 * 16 * 8] = part[1];
         }
+        __syncthreads();
+        v4f sum[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int st = 0; st < steps; ++st) {
+            Vec<T> columns[8];
+            if (st > 0) load_rows<T>(Mg, len, r, st, q, mcol, rows);
+            transpose8<T>(rows, columns);
+            const Vec<T> p = load16(parts + (st * 64 + lane) * 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[j], sum[j]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float factor = factor_of(f, exps[q * 4 + e]);
+            Vec<T> y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(sum[j][e], factor, to_float<T>(b[e][j])));
+            if (at[e] >= 0) *reinterpret_cast<Vec<T>*>(out + static_cast<int64_t>(at[e]) * ldo + col) = y;
+        }
     }
-    __syncthreads();
-    const float f = g < 0 ? 0.0f : scale[g];
-    float factor[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) factor[e] = factor_of(f, exps[q * 4 + e]);
-    if (inside && out != base) {         // rows without an adapter are base's
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (touched & none & 1ull << (q * 4 + e))
-                *reinterpret_cast<Vec<T>*>(piece_of(out, first, q, e, ldo, col)) = b[e];
-    }
-    if (g < 0) return;
-    v4f sum[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int st = 0; st < steps; ++st) {
-        Vec<T> columns[8];
-        if (st > 0) load_rows<T>(Mg, len, r, st, q, mcol, rows);
-        transpose8<T>(rows, columns);
-        const Vec<T> p = load16(parts + (st * 64 + lane) * 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[j], sum[j]);
-    }
-    if (inside) store_sums<T>(out, first, ldo, col, q, tokens, b, sum, factor);
 }
 
 // Joins the splits of P for many tokens, 16 lanes a token: T (fp32) and, laid
@@ -498,7 +618,10 @@ __global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict_
 // this one's sums are formed. M's operands stay for as long as the adapter
 // does not change: up to 32 ranks (ST steps of 16) in registers, up to 64 in
 // LDS, each wavefront its own. Beyond (ST = 0) they are read again for each
-// tile.
+// tile. Bound by memory: 4096 x 36864, rank 16: 107 us for 604 MB, 5.7 TB/s;
+// 4096 x 12288, rank 64: 56 us for 303 MB, 5.4 TB/s (167 us with those operands
+// in registers, which do not hold them). With the columns as the instruction's
+// rows, where a wavefront's access is 16 rows of 64 bytes, rank 16 took 138 us.
 template <typename T, int ST>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restrict__ parts,
                                                                const int32_t* __restrict__ exps,
@@ -951,6 +1074,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
 // More ranks: the wavefronts divide the ranks (RW tiles of 16 each). Each
 // reads and turns one tile of a round of four and leaves it in LDS for all, so
 // that Z is read once and every wavefront has rows of its own on their way.
+// 4096 tokens x (12288 + 36864), rank 64: 90-107 us for 403 MB and 50 MB of
+// partial sums, up to 4.9 TB/s (with a wavefront's own rows 171 us, with pairs
+// that read the same rows 148). It starts with the columns that the dot product
+// before it read last, which a cache may still hold: 94 us instead of 107.
 template <typename T, int RW>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_grad_shared(Side x, Side y, int r, Plan plan) {
     __shared__ Vec<T> turned[kWaves][8][64];
@@ -1026,49 +1153,60 @@ __global__ __launch_bounds__(kThreads) void k_lora_grad_sum(Side x, Side y, int 
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Few tokens most likely carry many adapters: small tiles, with blocks for
-// each adapter of a tile. With many, most tiles have one: where a pass does
-// not take two of them, the second has a block of its own, which leaves at
-// once in all other tiles (4096 x 36864, rank 64, two adapters that meet
-// inside a tile: 145 us for the one block's two passes, 107 for two blocks).
-bool few(int64_t s) { return s <= 256; }
-int slots_for(int64_t s, int64_t r) { return few(s) ? 16 : s <= 1024 ? 4 : r > 32 ? 2 : 1; }
+// Few tokens, as in decoding, may each carry an adapter of their own: blocks
+// for each adapter. With many, a block takes a tile of neighbours, most of
+// which have one adapter; where a pass does not take two of them, the second
+// has a block of its own, which leaves at once in all other tiles (4096 x
+// 36864, rank 64, two adapters that meet inside a tile: 145 us for the one
+// block's two passes, 107 for two blocks).
+bool few(int64_t s) { return s <= kFew; }
+int tile_slots(int64_t s, int64_t r) { return s <= 1024 ? 4 : r > 32 ? 2 : 1; }
+int few_slots(int64_t s, int64_t G) { return static_cast<int>(G < s ? G : s); }
+// blocks that share an adapter's tokens, in case they are all of one
+int few_spread(int64_t s) { return static_cast<int>(up(s, 64)); }
 
 // Parts that dot splits len into; each wavefront keeps at least two steps of
-// 64. Few tokens: two blocks for each, in case each has an adapter of its own.
-// Many: about one block a CU (4096 x 36864, rank 64: 69 us at 256 blocks, 78
-// at 512, 87 at 1024; where tiles with two adapters add a few blocks, 107 at
-// 256 and 112 at 448).
+// 64. Few tokens: 8 to 16, so that one adapter alone has blocks enough. Many:
+// about one block a CU (4096 x 36864, rank 64: 69 us at 256 blocks, 78 at 512,
+// 87 at 1024; where tiles with two adapters add a few blocks, 107 at 256 and
+// 112 at 448).
 int dot_splits(int64_t s, int64_t len, int64_t r) {
-    const int64_t most = len / 64 / 8;
-    int64_t n = few(s) ? up(2 * kCus, s > 0 ? s : 1) : up(kCus, up(s, r > 64 ? 32 : 64));
-    if (few(s)) n = n < 4 ? 4 : n > 16 ? 16 : n;
-    n = n < most ? n : most;
+    const int64_t most = len / 64 / 8, tok = r > 64 ? 32 : 64;
+    const int64_t want = few(s) ? (s <= 16 ? 16 : 8) : up(kCus, up(s, tok));
+    const int64_t n = want < most ? want : most;
     return static_cast<int>(n < 1 ? 1 : n);
 }
 
 template <typename T>
-hipError_t dot(const LoraArgs& a, const void* Z, int64_t ldz, const void* M, int64_t len, float* P,
+hipError_t dot(const LoraArgs& a, const void* Zv, int64_t ldz, const void* Mv, int64_t len, float* P,
                hipStream_t stream) {
-    const auto go = [&](auto mt, auto rt, auto na) {
-        constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NA = decltype(na)::value;
-        const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = slots_for(a.s, a.r);
-        const int splits = dot_splits(a.s, len, a.r);
-        k_lora_dot<T, MT, RT, NA><<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0,
-                                   stream>>>(static_cast<const T*>(Z), ldz, static_cast<const T*>(M), a.G, a.r,
-                                             static_cast<int>(len), a.ids, a.s, tiles, slots, splits, P);
-    };
+    const T* Z = static_cast<const T*>(Zv);
+    const T* M = static_cast<const T*>(Mv);
+    const int splits = dot_splits(a.s, len, a.r), n = static_cast<int>(len);
     using std::integral_constant;
     const integral_constant<int, 1> one;
     const integral_constant<int, 2> two;
     const integral_constant<int, 4> four;
     const integral_constant<int, 8> eight;
-    if (few(a.s)) {                      // a block has at most one adapter
-        if (a.r <= 16) go(one, one, one);
-        else if (a.r <= 32) go(one, two, one);
-        else if (a.r <= 64) go(one, four, one);
-        else go(one, eight, one);
+    if (few(a.s)) {
+        const int slots = few_slots(a.s, a.G), spread = few_spread(a.s);
+        const auto go = [&](auto rt) {
+            k_lora_dot_few<T, decltype(rt)::value>
+                <<<static_cast<unsigned>((slots + 1) * spread * splits), kThreads, 0, stream>>>(
+                    Z, ldz, M, a.G, a.r, n, a.ids, static_cast<int>(a.s), slots, spread, splits, P);
+        };
+        if (a.r <= 16) go(one);
+        else if (a.r <= 32) go(two);
+        else if (a.r <= 64) go(four);
+        else go(eight);
     } else {                             // as many adapters a pass as the registers hold
+        const auto go = [&](auto mt, auto rt, auto na) {
+            constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NA = decltype(na)::value;
+            const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = tile_slots(a.s, a.r);
+            k_lora_dot<T, MT, RT, NA>
+                <<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0, stream>>>(
+                    Z, ldz, M, a.G, a.r, n, a.ids, a.s, tiles, slots, splits, P);
+        };
         if (a.r <= 16) go(four, one, two);
         else if (a.r <= 32) go(four, two, two);
         else if (a.r <= 64) go(four, four, one);
@@ -1136,9 +1274,11 @@ hipError_t forward(const LoraArgs& a, const void* X, int64_t ldx, const void* ba
     hipError_t e = dot<T>(a, X, ldx, a.A, a.h, P, stream);
     if (e != hipSuccess) return e;
     if (few(a.s)) {
-        k_lora_add_few<T><<<static_cast<unsigned>(up(a.s, 16) * 16 * up(a.o, kAddColumns)), kThreads, 0, stream>>>(
-            P, splits, static_cast<const T*>(a.B), a.G, a.r, static_cast<int>(a.o), a.ids, a.scale,
-            static_cast<const T*>(base), ldb, static_cast<T*>(Y), ldy, a.s, Tp);
+        const int slots = few_slots(a.s, a.G), spread = few_spread(a.s);
+        k_lora_add_few<T>
+            <<<static_cast<unsigned>((slots + 1) * spread * up(a.o, kAddColumns)), kThreads, 0, stream>>>(
+                P, splits, static_cast<const T*>(a.B), a.G, a.r, static_cast<int>(a.o), a.ids, a.scale,
+                static_cast<const T*>(base), ldb, static_cast<T*>(Y), ldy, static_cast<int>(a.s), slots, spread, Tp);
         return hipGetLastError();
     }
     int32_t* exps = reinterpret_cast<int32_t*>(ws + d.exps);

@@ -122,7 +122,8 @@ SHAPES = [  # s, h, o, r, G, ids
     (65, 512, 576, 64, 2, "odd"), (129, 576, 320, 100, 3, "runs"), (300, 768, 704, 8, 4, "runs"),
     (511, 256, 256, 32, 2, "one"), (700, 320, 192, 12, 9, "mixed"), (1030, 128, 64, 127, 1, "odd"),
     (2100, 64, 128, 4, 300, "mixed"), (260, 4160, 4224, 16, 3, "runs"), (400, 1088, 640, 64, 3, "runs"),
-    (330, 320, 2112, 48, 2, "mixed"), (1100, 2048, 1024, 64, 1, "one"),
+    (330, 320, 2112, 48, 2, "mixed"), (1100, 2048, 1024, 64, 1, "one"), (256, 128, 576, 20, 2, "mixed"),
+    (255, 192, 64, 8, 300, "mixed"), (257, 1024, 192, 40, 6, "odd"), (256, 640, 64, 70, 1, "one"),
 ]
 
 
