@@ -190,10 +190,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     __shared__ v4f join[2][MT * RT * NA][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
     // Neighbouring blocks go to different XCDs, so a slot's blocks are neighbours:
-    // most of the higher slots' have nothing to do. Those that do start first,
-    // since they end last.
+    // most of the higher slots' have nothing to do.
     const int tile = blockIdx.x % tiles, part = blockIdx.x / tiles % splits;
-    const int slot = slots - 1 - blockIdx.x / tiles / splits;
+    const int slot = blockIdx.x / tiles / splits;
     const int64_t first = static_cast<int64_t>(tile) * TOK;
     const int steps = len / 64, w = part * kWaves + wave, all = splits * kWaves;
     const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w / all) * 64;
@@ -578,12 +577,12 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
 // out as add takes them, the two parts: [tile of 16][step][eight ranks of a
 // part][token][8], with the exponent of each token.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, int splits, int r, int64_t s,
-                                                        float* __restrict__ Tout, T* __restrict__ parts,
-                                                        int32_t* __restrict__ exps) {
+__device__ __forceinline__ void join_tile(const float* __restrict__ P, int splits, int r, int64_t s, int64_t tile,
+                                          float* __restrict__ Tout, T* __restrict__ parts,
+                                          int32_t* __restrict__ exps) {
     constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
-    const int steps = (r + 15) / 16, t = threadIdx.x / 16, sub = threadIdx.x % 16;
-    const int64_t tile = blockIdx.x, i = tile * 16 + t;
+    const int steps = (r + 15) / 16, t = threadIdx.x / 16 % 16, sub = threadIdx.x % 16;
+    const int64_t i = tile * 16 + t;
     float v[kSteps], most = 0.0f;
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
@@ -611,6 +610,13 @@ __global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict_
         to[0] = part[0];
         to[2 * 16 * 8] = part[1];
     }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, int splits, int r, int64_t s,
+                                                        float* __restrict__ Tout, T* __restrict__ parts,
+                                                        int32_t* __restrict__ exps) {
+    join_tile(P, splits, r, s, blockIdx.x, Tout, parts, exps);
 }
 
 // Many tokens: a block takes 512 columns and `run` tiles of 16 tokens one
@@ -760,8 +766,7 @@ constexpr int kPlanThreads = 1024;
 // partial sums, if it has more than one chunk, at 2 C / KC: each leaves the
 // adapters room whatever their counts, without one block knowing the others'.
 // Unused entries up to the next adapter's are marked by this one.
-__global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __restrict__ ids, int s, int G, int KC,
-                                                            Plan plan) {
+__device__ __forceinline__ void plan_adapter(const int32_t* __restrict__ ids, int s, int G, int KC, const Plan& plan) {
     constexpr int W = kPlanThreads / 64;
     __shared__ int counts[4][W];
     __shared__ uint32_t seen[2048];
@@ -838,6 +843,22 @@ __global__ __launch_bounds__(kPlanThreads) void k_lora_plan(const int32_t* __res
         if (mine) plan.order[at + __popcll(vote & ((1ull << lane) - 1))] = i;
         before += all;
     }
+}
+
+// The plan needs nothing of the dot product and the join nothing of the plan:
+// one launch for both, the first G blocks for the plan (4096 tokens, rank 64:
+// 9 us instead of 8 and 5).
+template <typename T>
+__global__ __launch_bounds__(kPlanThreads) void k_lora_plan_join(const int32_t* __restrict__ ids, int s, int G, int KC,
+                                                                 Plan plan, const float* __restrict__ P, int splits,
+                                                                 int r, float* __restrict__ dT, T* __restrict__ parts,
+                                                                 int32_t* __restrict__ exps) {
+    if (blockIdx.x < static_cast<unsigned>(G)) {
+        plan_adapter(ids, s, G, KC, plan);
+        return;
+    }
+    const int64_t tile = static_cast<int64_t>(blockIdx.x - G) * (kPlanThreads / 256) + threadIdx.x / 256;
+    if (tile * 16 < s) join_tile(P, splits, r, s, tile, dT, parts, exps);
 }
 
 // One of the two gradients: the streamed rows Z, the fp32 factors P [s, r] and
@@ -1015,12 +1036,28 @@ struct GradBlock {
     }
 };
 
+// Blocks past those of the chunks, one for each adapter and 128 columns, write
+// the zeros of adapters that no token carries. True for such a block.
+__device__ __forceinline__ bool write_zeros(const Side& x, const Side& y, int r, const Plan& plan) {
+    const int xblocks = (x.len + 127) / 128, blocks = xblocks + (y.len + 127) / 128;
+    if (blockIdx.x < static_cast<unsigned>(plan.slots) * blocks) return false;
+    const int at = blockIdx.x - plan.slots * blocks, g = at / blocks, cb = at % blocks;
+    if (plan.count[g] > 0) return true;
+    const bool second = cb >= xblocks;
+    const int len = second ? y.len : x.len, col = (second ? cb - xblocks : cb) * 128 + (threadIdx.x & 31) * 4;
+    float* out = (second ? y.out : x.out) + static_cast<int64_t>(g) * r * len;
+    for (int k = threadIdx.x >> 5; k < r && col < len; k += kThreads / 32)
+        *reinterpret_cast<v4f*>(out + static_cast<int64_t>(k) * len + col) = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    return true;
+}
+
 // Up to 32 ranks (RT tiles): every wavefront takes all ranks and every fourth
 // tile, with the next one's rows, and the tokens of the one after, on their
 // way while this one's sums are formed; the four sums are joined in LDS.
 template <typename T, int RT>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
     __shared__ v4f join[2][RT * 8][64];
+    if (write_zeros(x, y, r, plan)) return;
     const GradBlock<T> b(x, y, r, plan);
     if (b.c.g < 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -1081,6 +1118,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
 template <typename T, int RW>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_grad_shared(Side x, Side y, int r, Plan plan) {
     __shared__ Vec<T> turned[kWaves][8][64];
+    if (write_zeros(x, y, r, plan)) return;
     const GradBlock<T> b(x, y, r, plan);
     if (b.c.g < 0) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -1294,8 +1332,10 @@ struct Layout {
     DotPlaces d;
 
     Layout(int64_t s, int64_t h, int64_t o, int64_t r, int64_t G) : d(w, s, o, r) {
-        // chunks as long as still leave about 1024 blocks, up to 1024 tiles
-        const int64_t blocks = up(h, 128) + up(o, 128);
+        // Chunks as long as still leave about 1024 blocks, up to 1024 tiles; for up
+        // to 512 tokens no partial sums, whose launch costs more than the blocks
+        // gain (301 tokens of three adapters, rank 8: 34.4 us with them, 30.0 without).
+        const int64_t blocks = s <= 512 ? 4 * kCus : up(h, 128) + up(o, 128);
         int64_t kc = up(up(s > 0 ? s : 1, up(4 * kCus, blocks)), 128) * 128;
         kc = kc < 32768 ? kc : 32768;
         KC = static_cast<int>(kc);
@@ -1333,21 +1373,26 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
     const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
     const int r = a.r;
-    k_lora_plan<<<static_cast<unsigned>(a.G), kPlanThreads, 0, stream>>>(a.ids, static_cast<int>(a.s),
-                                                                        static_cast<int>(a.G), l.KC, plan);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    float* P = floats(l.d.P);
+    const auto plan_join = [&] {
+        k_lora_plan_join<T>
+            <<<static_cast<unsigned>(a.G + up(a.s, kPlanThreads / 16)), kPlanThreads, 0, stream>>>(
+                a.ids, static_cast<int>(a.s), static_cast<int>(a.G), l.KC, plan, P, dot_splits(a.s, a.o, r), r, dT,
+                reinterpret_cast<T*>(ws + l.d.parts), ints(l.d.exps));
+        return hipGetLastError();
+    };
+    hipError_t e;
     if (a.s > 0) {
-        float* P = floats(l.d.P);
         if ((e = dot<T>(a, dY, lddy, a.B, a.o, P, stream)) != hipSuccess) return e;
-        if ((e = join<T>(a, dot_splits(a.s, a.o, r), P, dT, ws + l.d.parts, ints(l.d.exps), stream)) != hipSuccess)
-            return e;
+        if ((e = plan_join()) != hipSuccess) return e;
         const dim3 per_tile(static_cast<unsigned>(l.tiles), static_cast<unsigned>(up(2 * rt, kWaves)));
         if constexpr (kScaled<T>)
             k_lora_most<<<per_tile, kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         k_lora_lay<T><<<per_tile, kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        const unsigned blocks = static_cast<unsigned>(l.slots * (up(a.h, 128) + up(a.o, 128)));
+        // without partial sums the same launch also writes the zeros
+        const unsigned blocks =
+            static_cast<unsigned>((l.slots + (l.KC < a.s ? 0 : a.G)) * (up(a.h, 128) + up(a.o, 128)));
         if (rt == 1) k_lora_grad<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
         else if (rt == 2) k_lora_grad<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
         else if (rt <= 4) k_lora_grad_shared<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
@@ -1357,6 +1402,8 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
                       hipSuccess)
             return e;
     }
+    if (a.s > 0 && l.KC >= a.s) return hipSuccess;
+    if (a.s == 0 && (e = plan_join()) != hipSuccess) return e;
     const int64_t fours = static_cast<int64_t>(r) * (a.h + a.o) / 4;
     k_lora_grad_sum<<<dim3(static_cast<unsigned>(up(fours, kThreads)), static_cast<unsigned>(a.G)), kThreads, 0,
                       stream>>>(x, y, r, l.KC, plan);
