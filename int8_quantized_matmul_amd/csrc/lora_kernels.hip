@@ -177,24 +177,33 @@ struct Adapters {
 // rows past the end are read from the last row and their sums dropped. Of the
 // tile's adapters the block takes every `slots`-th, and up to NA of them in
 // one pass over Z: a tile where one request ends and the next begins costs no
-// second pass. Bound by memory up to 32 ranks (4096 x 12288, rank 16: 24-30 us,
+// second pass. Where the registers hold one (NA = 1), slot 0 takes the tile's
+// first adapter and the others the rest, in `late` parts instead of `splits`:
+// they are few, and as long as slot 0's they would be what the launch waits
+// for. Bound by memory up to 32 ranks (4096 x 12288, rank 16: 24-30 us,
 // 3.4-4.2 TB/s, 20 for one adapter) and by the CU's loads beyond, where M's
 // pieces are as many as Z's (4096 x 36864, rank 64: 69 us for one adapter, 4.4
 // TB/s). The next step's loads go before this one's sums (78 us without).
+__host__ __device__ constexpr int dot_tokens(int r) { return r > 64 ? 32 : 64; }
+
 template <typename T, int MT, int RT, int NA>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ Z, int64_t ldz,
                                                           const T* __restrict__ M, int64_t G, int r, int len,
                                                           const int32_t* __restrict__ ids, int64_t s, int tiles,
-                                                          int slots, int splits, float* __restrict__ P) {
+                                                          int slots, int splits, int late,
+                                                          float* __restrict__ P) {
     constexpr int TOK = 16 * MT;
     __shared__ v4f join[2][MT * RT * NA][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-    // Neighbouring blocks go to different XCDs, so a slot's blocks are neighbours:
-    // most of the higher slots' have nothing to do.
-    const int tile = blockIdx.x % tiles, part = blockIdx.x / tiles % splits;
-    const int slot = blockIdx.x / tiles / splits;
+    // Neighbouring blocks go to different XCDs, so a slot's blocks are neighbours,
+    // most of the higher slots' having nothing to do, and a tile's parts are: those
+    // of a tile with two adapters on one XCD took 107 us instead of 95.
+    const int later = static_cast<int>(blockIdx.x) - tiles * splits;      // blocks past slot 0's
+    const int slot = later < 0 ? 0 : 1 + later / (tiles * late), parts = slot == 0 ? splits : late;
+    const int nth = slot == 0 ? static_cast<int>(blockIdx.x) : later % (tiles * late);
+    const int part = nth % parts, tile = nth / parts;
     const int64_t first = static_cast<int64_t>(tile) * TOK;
-    const int steps = len / 64, w = part * kWaves + wave, all = splits * kWaves;
+    const int steps = len / 64, w = part * kWaves + wave, all = parts * kWaves;
     const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w / all) * 64;
     const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (w + 1) / all) * 64;
     P += static_cast<int64_t>(part) * s * r;
@@ -297,7 +306,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_dot(const T* __restrict__ 
     for (int turn = 0; adapters.left; ++turn) {
         uint64_t mine;
         const int64_t id = adapters.next(mine);
-        if (turn % slots != slot) continue;
+        if ((NA == 2 ? turn % slots : turn == 0 ? 0 : 1 + (turn - 1) % (slots - 1)) != slot) continue;
         if (NA == 2 && held == 0) {
             g[0] = id;
             tokens[0] = mine;
@@ -576,13 +585,28 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
 // Joins the splits of P for many tokens, 16 lanes a token: T (fp32) and, laid
 // out as add takes them, the two parts: [tile of 16][step][eight ranks of a
 // part][token][8], with the exponent of each token.
+// A token whose adapter is not the first of its tile in dot has `late` splits.
+__device__ __forceinline__ int splits_of(const int32_t* __restrict__ ids, int64_t G, int splits, int late, int r,
+                                         int64_t s, int64_t i) {
+    if (late == splits) return splits;
+    const int tok = dot_tokens(r), lane = threadIdx.x & 63;
+    const int64_t first = i / tok * tok, at = first + lane % tok;
+    int id = at < s ? ids[at] : -1;
+    if (id < 0 || id >= G) id = -1;
+    const uint64_t some = __ballot(id >= 0);
+    const int own = __shfl(id, static_cast<int>(i - first), kWave);
+    return own >= 0 && own != __builtin_amdgcn_readlane(id, __builtin_ctzll(some)) ? late : splits;
+}
+
 template <typename T>
-__device__ __forceinline__ void join_tile(const float* __restrict__ P, int splits, int r, int64_t s, int64_t tile,
+__device__ __forceinline__ void join_tile(const float* __restrict__ P, const int32_t* __restrict__ ids, int64_t G,
+                                          int splits, int late, int r, int64_t s, int64_t tile,
                                           float* __restrict__ Tout, T* __restrict__ parts,
                                           int32_t* __restrict__ exps) {
     constexpr int kSteps = I8MM_LORA_MAX_RANK / 16;
     const int steps = (r + 15) / 16, t = threadIdx.x / 16 % 16, sub = threadIdx.x % 16;
     const int64_t i = tile * 16 + t;
+    const int mine = splits_of(ids, G, splits, late, r, s, i);
     float v[kSteps], most = 0.0f;
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
@@ -590,7 +614,7 @@ __device__ __forceinline__ void join_tile(const float* __restrict__ P, int split
         if (st >= steps) continue;
         const int k = st * 16 + sub;
         const bool real = i < s && k < r;
-        const float sum = join_splits(P + (real ? i * r + k : 0), s * r, splits);
+        const float sum = join_splits(P + (real ? i * r + k : 0), s * r, mine);
         if (real) {
             v[st] = sum;
             if (Tout) Tout[i * r + k] = sum;
@@ -613,10 +637,11 @@ __device__ __forceinline__ void join_tile(const float* __restrict__ P, int split
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, int splits, int r, int64_t s,
+__global__ __launch_bounds__(kThreads) void k_lora_join(const float* __restrict__ P, const int32_t* __restrict__ ids,
+                                                        int64_t G, int splits, int late, int r, int64_t s,
                                                         float* __restrict__ Tout, T* __restrict__ parts,
                                                         int32_t* __restrict__ exps) {
-    join_tile(P, splits, r, s, blockIdx.x, Tout, parts, exps);
+    join_tile(P, ids, G, splits, late, r, s, blockIdx.x, Tout, parts, exps);
 }
 
 // Many tokens: a block takes 512 columns and `run` tiles of 16 tokens one
@@ -851,14 +876,14 @@ __device__ __forceinline__ void plan_adapter(const int32_t* __restrict__ ids, in
 template <typename T>
 __global__ __launch_bounds__(kPlanThreads) void k_lora_plan_join(const int32_t* __restrict__ ids, int s, int G, int KC,
                                                                  Plan plan, const float* __restrict__ P, int splits,
-                                                                 int r, float* __restrict__ dT, T* __restrict__ parts,
+                                                                 int late, int r, float* __restrict__ dT, T* __restrict__ parts,
                                                                  int32_t* __restrict__ exps) {
     if (blockIdx.x < static_cast<unsigned>(G)) {
         plan_adapter(ids, s, G, KC, plan);
         return;
     }
     const int64_t tile = static_cast<int64_t>(blockIdx.x - G) * (kPlanThreads / 256) + threadIdx.x / 256;
-    if (tile * 16 < s) join_tile(P, splits, r, s, tile, dT, parts, exps);
+    if (tile * 16 < s) join_tile(P, ids, G, splits, late, r, s, tile, dT, parts, exps);
 }
 
 // One of the two gradients: the streamed rows Z, the fp32 factors P [s, r] and
@@ -1193,10 +1218,10 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Few tokens, as in decoding, may each carry an adapter of their own: blocks
 // for each adapter. With many, a block takes a tile of neighbours, most of
-// which have one adapter; where a pass does not take two of them, the second
-// has a block of its own, which leaves at once in all other tiles (4096 x
+// which have one adapter; where a pass does not take two of them, the others
+// have blocks of their own, which leave at once in all other tiles (4096 x
 // 36864, rank 64, two adapters that meet inside a tile: 145 us for the one
-// block's two passes, 107 for two blocks).
+// block's two passes, 115 for two blocks, 89 with the second in smaller parts).
 bool few(int64_t s) { return s <= kFew; }
 int tile_slots(int64_t s, int64_t r) { return s <= 1024 ? 4 : r > 32 ? 2 : 1; }
 int few_slots(int64_t s, int64_t G) { return static_cast<int>(G < s ? G : s); }
@@ -1206,13 +1231,21 @@ int few_spread(int64_t s) { return static_cast<int>(up(s, 64)); }
 // Parts that dot splits len into; each wavefront keeps at least two steps of
 // 64. Few tokens: 8 to 16, so that one adapter alone has blocks enough. Many:
 // about one block a CU (4096 x 36864, rank 64: 69 us at 256 blocks, 78 at 512,
-// 87 at 1024; where tiles with two adapters add a few blocks, 107 at 256 and
-// 112 at 448).
+// 87 at 1024).
 int dot_splits(int64_t s, int64_t len, int64_t r) {
-    const int64_t most = len / 64 / 8, tok = r > 64 ? 32 : 64;
-    const int64_t want = few(s) ? (s <= 16 ? 16 : 8) : up(kCus, up(s, tok));
+    const int64_t most = len / 64 / 8;
+    const int64_t want = few(s) ? (s <= 16 ? 16 : 8) : up(kCus, up(s, dot_tokens(static_cast<int>(r))));
     const int64_t n = want < most ? want : most;
     return static_cast<int>(n < 1 ? 1 : n);
+}
+
+// Parts for a tile's later adapters, where a pass takes one adapter. 4096 x
+// 36864, rank 64, one tile with two adapters: 115 us with as many parts as the
+// first has, 95 with 16, 89 with 32, 83 without such a tile; rank 128, four
+// such tiles: 223, 174, 164.
+int dot_late(int splits, int64_t r) {
+    const int n = 8 * splits < 32 ? 8 * splits : 32;
+    return r <= 32 || splits > n ? splits : n;
 }
 
 template <typename T>
@@ -1220,7 +1253,7 @@ hipError_t dot(const LoraArgs& a, const void* Zv, int64_t ldz, const void* Mv, i
                hipStream_t stream) {
     const T* Z = static_cast<const T*>(Zv);
     const T* M = static_cast<const T*>(Mv);
-    const int splits = dot_splits(a.s, len, a.r), n = static_cast<int>(len);
+    const int splits = dot_splits(a.s, len, a.r), late = dot_late(splits, a.r), n = static_cast<int>(len);
     using std::integral_constant;
     const integral_constant<int, 1> one;
     const integral_constant<int, 2> two;
@@ -1242,8 +1275,8 @@ hipError_t dot(const LoraArgs& a, const void* Zv, int64_t ldz, const void* Mv, i
             constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NA = decltype(na)::value;
             const int tiles = static_cast<int>(up(a.s, 16 * MT)), slots = tile_slots(a.s, a.r);
             k_lora_dot<T, MT, RT, NA>
-                <<<static_cast<unsigned>(static_cast<int64_t>(tiles) * slots * splits), kThreads, 0, stream>>>(
-                    Z, ldz, M, a.G, a.r, n, a.ids, a.s, tiles, slots, splits, P);
+                <<<static_cast<unsigned>(tiles * (splits + (slots - 1) * static_cast<int64_t>(late))), kThreads, 0,
+                   stream>>>(Z, ldz, M, a.G, a.r, n, a.ids, a.s, tiles, slots, splits, late, P);
         };
         if (a.r <= 16) go(four, one, two);
         else if (a.r <= 32) go(four, two, two);
@@ -1287,7 +1320,8 @@ struct Places {
 struct DotPlaces {
     size_t P, parts, exps;
     DotPlaces(Places& w, int64_t s, int64_t len, int64_t r) {
-        P = w.take(4 * dot_splits(s, len, r) * s * r);
+        const int splits = dot_splits(s, len, r);
+        P = w.take(4 * (few(s) ? splits : dot_late(splits, r)) * s * r);
         parts = w.take(up(s, 16) * up(r, 16) * 16 * 32 * 2);
         exps = w.take(4 * up(s, 16) * 16);
     }
@@ -1296,8 +1330,8 @@ struct DotPlaces {
 template <typename T>
 hipError_t join(const LoraArgs& a, int splits, const float* P, float* Tout, void* parts, int32_t* exps,
                 hipStream_t stream) {
-    k_lora_join<T><<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(P, splits, a.r, a.s, Tout,
-                                                                               static_cast<T*>(parts), exps);
+    k_lora_join<T><<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(
+        P, a.ids, a.G, splits, dot_late(splits, a.r), a.r, a.s, Tout, static_cast<T*>(parts), exps);
     return hipGetLastError();
 }
 
@@ -1374,10 +1408,11 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
     const int r = a.r;
     float* P = floats(l.d.P);
+    const int splits = dot_splits(a.s, a.o, a.r), late = few(a.s) ? splits : dot_late(splits, a.r);
     const auto plan_join = [&] {
         k_lora_plan_join<T>
             <<<static_cast<unsigned>(a.G + up(a.s, kPlanThreads / 16)), kPlanThreads, 0, stream>>>(
-                a.ids, static_cast<int>(a.s), static_cast<int>(a.G), l.KC, plan, P, dot_splits(a.s, a.o, r), r, dT,
+                a.ids, static_cast<int>(a.s), static_cast<int>(a.G), l.KC, plan, P, splits, late, r, dT,
                 reinterpret_cast<T*>(ws + l.d.parts), ints(l.d.exps));
         return hipGetLastError();
     };

@@ -124,6 +124,7 @@ SHAPES = [  # s, h, o, r, G, ids
     (2100, 64, 128, 4, 300, "mixed"), (260, 4160, 4224, 16, 3, "runs"), (400, 1088, 640, 64, 3, "runs"),
     (330, 320, 2112, 48, 2, "mixed"), (1100, 2048, 1024, 64, 1, "one"), (256, 128, 576, 20, 2, "mixed"),
     (255, 192, 64, 8, 300, "mixed"), (257, 1024, 192, 40, 6, "odd"), (256, 640, 64, 70, 1, "one"),
+    (1500, 1024, 4160, 64, 5, "runs"), (2050, 2048, 1088, 96, 4, "mixed"), (1111, 4096, 256, 40, 20, "odd"),
 ]
 
 
