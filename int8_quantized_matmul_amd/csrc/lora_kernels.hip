@@ -16,8 +16,10 @@
 // Precision. P (T, dT) is summed and kept in fp32. Where it meets 16-bit
 // values in a matrix instruction it is carried as a sum of 16-bit parts,
 // multiplied one after another into the same fp32 sum. fp16: two parts of 11
-// bits, after an exact power of two has brought the largest of the values
-// that share it near 2^14, so that neither range nor subnormals cost digits;
+// bits, after an exact power of two has brought the largest finite one of the
+// values that share it near 2^14 (in Y and dX a token's ranks share it, in dA
+// and dB the tokens of a chunk, each rank for itself); a value is then off by
+// at most 2^-23 of itself or 2^-39 of that largest one, whichever is more.
 // bf16, which has fp32's range: two parts of 8 bits towards a 16-bit result,
 // three towards an fp32 one. Y and dX are rounded once.
 
@@ -84,23 +86,27 @@ __device__ __forceinline__ void transpose8(const Vec<T>(&rows)[8], Vec<T>(&colum
     for (int j = 0; j < 8; ++j) columns[j] = __builtin_bit_cast(Vec<T>, out[j]);
 }
 
-// The power of two that takes values up to `most` in magnitude near 2^14, as
-// its exponent; 0 for none, for infinity and for NaN.
+// The power of two that takes finite values up to `most` in magnitude near
+// 2^14, as its exponent; 0 if there are none.
 template <typename T>
 __device__ __forceinline__ int scale_exponent(float most) {
     if constexpr (!kScaled<T>) return 0;
-    return most > 0.0f && most < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+    return most > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+}
+
+// What a value counts for in the largest of those that share a power of two:
+// infinity and NaN, which no power of two changes, count for nothing, so that
+// they cost the finite values beside them no digits.
+__device__ __forceinline__ float finite_size(float v) {
+    const float size = fabsf(v);
+    return size < __builtin_inff() ? size : 0.0f;
 }
 
 // v 2^ex as a sum of N parts of type T. What is not finite is its own first
-// part; a finite value that fp16 cannot hold (beside an infinity, which left
-// ex at 0) stays finite.
+// part.
 template <typename T, int N>
 __device__ __forceinline__ void split(float v, int ex, T(&part)[N]) {
-    if constexpr (kScaled<T>) {
-        v = ldexpf(v, ex);
-        if (fabsf(v) < __builtin_inff()) v = fminf(fmaxf(v, -65504.0f), 65504.0f);
-    }
+    if constexpr (kScaled<T>) v = ldexpf(v, ex);
     const bool finite = fabsf(v) < __builtin_inff();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -542,8 +548,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
             const float sum = join_splits(P + (real ? it * r + k : 0), static_cast<int64_t>(s) * r, splits);
             if (real && Tout && cb == 0) Tout[it * r + k] = sum;
             values[t][k] = real ? sum : 0.0f;
-            // NaN counts as infinity: no power of two for the row
-            if (real) most = fmaxf(most, sum == sum ? fabsf(sum) : __builtin_inff());
+            if (real) most = fmaxf(most, finite_size(sum));
         }
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
@@ -619,7 +624,7 @@ __device__ __forceinline__ void join_tile(const float* __restrict__ P, const int
             v[st] = sum;
             if (Tout) Tout[i * r + k] = sum;
         }
-        most = fmaxf(most, v[st] == v[st] ? fabsf(v[st]) : __builtin_inff());
+        most = fmaxf(most, finite_size(v[st]));
     }
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, kWave));
@@ -779,7 +784,8 @@ struct Plan {
     int32_t* part;                   // [G]: its first partial sums
     int32_t* tile_chunk;             // [tiles]: the chunk of each tile, or -1
     Chunk* chunks;                   // [slots]
-    float* most;                     // [2 rank tiles][tiles]: the largest |factor|
+    float* most;                     // [2 rank tiles][tiles][16]: each rank's largest finite |factor|
+    int32_t* exps;                   // [slots][2 rank tiles][16]: the power of two of each chunk and rank
     int slots, tiles, rank_tiles;
 };
 
@@ -924,9 +930,14 @@ struct TileFactors {
     }
 };
 
-// The largest |f_g P| of each tile and 16 ranks, for both sides: a block takes
-// one tile, a wavefront one task (16 ranks of one side). NaN counts as
-// infinity.
+// The largest finite value in the four lanes of each rank, in all of them.
+__device__ __forceinline__ float rank_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, kWave));
+    return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+
+// The largest finite |f_g P| of each tile and rank, for both sides: a block
+// takes one tile, a wavefront one task (16 ranks of one side).
 __global__ __launch_bounds__(kThreads) void k_lora_most(Side x, Side y, const float* __restrict__ scale, int r,
                                                         Plan plan) {
     const int chunk = plan.tile_chunk[blockIdx.x], tasks = 2 * plan.rank_tiles;
@@ -937,19 +948,23 @@ __global__ __launch_bounds__(kThreads) void k_lora_most(Side x, Side y, const fl
     float v[8], most = 0.0f;
     t.load(which ? y.P : x.P, rt * 16 + (threadIdx.x & 15), r, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = fmaxf(most, v[e] == v[e] ? fabsf(v[e]) : __builtin_inff());
-    most = wave_max(most);
-    if ((threadIdx.x & 63) == 0) plan.most[static_cast<int64_t>(task) * plan.tiles + blockIdx.x] = most;
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_size(v[e]));
+    most = rank_max(most);
+    if ((threadIdx.x & 63) < 16)
+        plan.most[(static_cast<int64_t>(task) * plan.tiles + blockIdx.x) * 16 + threadIdx.x % 16] = most;
 }
 
-// The power of two of a chunk and task, from all its tiles.
+// The power of two of a chunk and rank task 16 + lane % 16, from all the
+// chunk's tiles. Ranks do not share theirs: one that is far smaller than its
+// neighbours, as a rank that has hardly been trained, keeps its digits.
 template <typename T>
 __device__ __forceinline__ int exponent_of(const Plan& plan, const Chunk& c, int task) {
     if constexpr (!kScaled<T>) return 0;
-    const float* at = plan.most + static_cast<int64_t>(task) * plan.tiles + c.tile;
+    const float* at = plan.most + (static_cast<int64_t>(task) * plan.tiles + c.tile) * 16;
     float most = 0.0f;
-    for (int st = threadIdx.x & 63; st < (c.count + 31) / 32; st += 64) most = fmaxf(most, at[st]);
-    return scale_exponent<T>(wave_max(most));
+#pragma unroll 8
+    for (int k = threadIdx.x & 63; k < (c.count + 31) / 32 * 16; k += 64) most = fmaxf(most, at[k]);
+    return scale_exponent<T>(rank_max(most));
 }
 
 // Lays f_g P out as the matrix instruction takes it: a block takes one tile, a
@@ -965,9 +980,11 @@ __global__ __launch_bounds__(kThreads) void k_lora_lay(Side x, Side y, const flo
     const int lane = threadIdx.x & 63, n = lane & 15;
     {
         const int which = task >= plan.rank_tiles, rt = which ? task - plan.rank_tiles : task;
-        const int ex = exponent_of<T>(plan, c, task);
         float v[8];
         t.load(which ? y.P : x.P, rt * 16 + n, r, v);
+        const int ex = exponent_of<T>(plan, c, task);
+        if (kScaled<T> && static_cast<int>(blockIdx.x) == c.tile && lane < 16)
+            plan.exps[(static_cast<int64_t>(chunk) * 2 * plan.rank_tiles + task) * 16 + lane] = ex;
         Vec<T> out[kParts<T>];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -1044,10 +1061,14 @@ struct GradBlock {
         for (int p = 0; p < kParts<T>; ++p) f[p] = load16(at + p * 512);
     }
     __device__ __forceinline__ void store(const Plan& plan, int rt, int r, const v4f(&sum)[8]) const {
-        const int ex = exponent_of<T>(plan, c, second * plan.rank_tiles + rt);
+        const int row = static_cast<int>(threadIdx.x >> 4 & 3) * 4;
+        v4i exs{0, 0, 0, 0};
+        if constexpr (kScaled<T>)
+            exs = *reinterpret_cast<const v4i*>(
+                plan.exps + (static_cast<int64_t>(chunk) * 2 * plan.rank_tiles + second * plan.rank_tiles + rt) * 16 + row);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int k = rt * 16 + static_cast<int>(threadIdx.x >> 4 & 3) * 4 + e;
+            const int k = rt * 16 + row + e, ex = exs[e];
             if (k >= r || col >= len) continue;
             v4f lo, hi;
 #pragma unroll
@@ -1364,7 +1385,7 @@ hipError_t forward(const LoraArgs& a, const void* X, int64_t ldx, const void* ba
 // The backward pass's workspace.
 struct Layout {
     int KC, slots, tiles;
-    size_t dT, order, count, part, tile_chunk, chunks, most, laid[2], sums[2];
+    size_t dT, order, count, part, tile_chunk, chunks, most, exps, laid[2], sums[2];
     Places w;
     DotPlaces d;
 
@@ -1386,7 +1407,8 @@ struct Layout {
         part = w.take(4 * G);
         tile_chunk = w.take(4 * tiles);
         chunks = w.take(static_cast<int64_t>(sizeof(Chunk)) * slots);
-        most = w.take(4 * 2 * rt * tiles);
+        most = w.take(4 * 2 * rt * tiles * 16);
+        exps = w.take(4 * 2 * rt * slots * 16);
         for (int k = 0; k < 2; ++k) {
             laid[k] = w.take(tiles * rt * 3 * 512 * 2);
             sums[k] = w.take(4 * parts * r * (k == 0 ? h : o));
@@ -1404,7 +1426,7 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const int rt = static_cast<int>(up(a.r, 16));
     const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
-                    reinterpret_cast<Chunk*>(ws + l.chunks), floats(l.most), l.slots,
+                    reinterpret_cast<Chunk*>(ws + l.chunks), floats(l.most), ints(l.exps), l.slots,
                     l.tiles, rt};
     float* dT = floats(l.dT);
     const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
