@@ -645,7 +645,7 @@ size_t i8mm_clip_grad_norm_workspace_bytes(const int64_t* numels, int64_t n);
  *   N = sqrt(sum of the squares of all elements of all tensors),
  *   out = c g with c = min(1, max_norm / (N + 1e-6)).
  * The squares are summed in fp64. A NaN in any gradient makes N, and with it
- * every output, NaN; an infinite one makes c = 0.
+ * every output, NaN; an infinite one makes c = 0, or 1 if max_norm is +inf.
  *
  * grads, outs: HOST arrays of n device pointers (outs may be NULL: the
  * gradients are scaled in place; outs[i] may be grads[i]); numels: host

@@ -853,7 +853,8 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     """The global norm N over all gradients (contiguous tensors on the current
     GPU, each fp16, bf16 or fp32), as fp32 [1] on the GPU, and the gradients
     times min(1, max_norm / (N + 1e-6)): in place, or into the tensors of
-    `out`, each of its gradient's size and type."""
+    `out`, each of its gradient's size and type. max_norm = inf leaves them as
+    they are, whatever N is but NaN."""
     grads = list(grads)
     n = len(grads)
     dev = torch.cuda.current_device()

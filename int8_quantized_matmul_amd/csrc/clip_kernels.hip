@@ -135,7 +135,9 @@ __global__ __launch_bounds__(kThreads) void k_clip_scale(const Batch b, const do
     const double norm = sqrt(block_sum_f64(sum, red));
     if (total && blockIdx.x == 0 && threadIdx.x == 0) total[0] = static_cast<float>(norm);
     const double ratio = max_norm / (norm + 1e-6);
-    const float c = ratio < 1.0 || ratio != ratio ? static_cast<float>(ratio) : 1.0f;   // a NaN reaches the gradients
+    // A NaN reaches the gradients; an infinite norm over an infinite limit, whose
+    // ratio is NaN too, leaves them alone.
+    const float c = norm != norm ? static_cast<float>(norm) : ratio < 1.0 ? static_cast<float>(ratio) : 1.0f;
     for (uint32_t k = blockIdx.x; k < b.chunks; k += gridDim.x) {
         const uint32_t chunk = b.chunks - 1 - k;
         const int tensor = tensor_of(b, chunk);

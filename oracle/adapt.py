@@ -63,9 +63,10 @@ def lora_backward(dY, X, T, A, B, ids, scale, base: Optional[np.ndarray]
 
 
 def clip_grad_norm(grads: Sequence[np.ndarray], max_norm: float) -> Tuple[float, List[np.ndarray]]:
-    """(N, the gradients times min(1, max_norm / (N + 1e-6)))."""
+    """(N, the gradients times min(1, max_norm / (N + 1e-6))); the factor is 1
+    if max_norm is infinite, whatever N is but NaN."""
     grads = [np.asarray(g, F) for g in grads]
     total = np.sqrt(sum(float(np.sum(g * g)) for g in grads))
-    c = max_norm / (total + 1e-6)
-    c = c if np.isnan(c) else min(1.0, c)
-    return float(total), [c * g for g in grads]
+    c = total if np.isnan(total) else 1.0 if np.isinf(max_norm) else min(1.0, max_norm / (total + 1e-6))
+    with np.errstate(invalid="ignore"):          # 0 times an infinity
+        return float(total), [c * g for g in grads]
