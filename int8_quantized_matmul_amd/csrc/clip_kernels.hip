@@ -135,16 +135,21 @@ __global__ __launch_bounds__(kThreads) void k_clip_scale(const Batch b, const do
     const double norm = sqrt(block_sum_f64(sum, red));
     if (total && blockIdx.x == 0 && threadIdx.x == 0) total[0] = static_cast<float>(norm);
     const double ratio = max_norm / (norm + 1e-6);
+    // A ratio below fp32's normal numbers, which gradients near fp32's upper end
+    // make of a small limit, is applied in two steps, the second a power of two.
+    const bool tiny = ratio < 0x1p-126;
+    const double up = tiny ? 0x1p126 : 1.0;
+    const float down = tiny ? 0x1p-126f : 1.0f;
     // A NaN reaches the gradients; an infinite norm over an infinite limit, whose
     // ratio is NaN too, leaves them alone.
-    const float c = norm != norm ? static_cast<float>(norm) : ratio < 1.0 ? static_cast<float>(ratio) : 1.0f;
+    const float c = norm != norm ? static_cast<float>(norm) : ratio < 1.0 ? static_cast<float>(ratio * up) : 1.0f;
     for (uint32_t k = blockIdx.x; k < b.chunks; k += gridDim.x) {
         const uint32_t chunk = b.chunks - 1 - k;
         const int tensor = tensor_of(b, chunk);
         const Piece p = piece_of(b, tensor, chunk);
         const void* in = b.in[tensor];
         void* out = b.out[tensor];
-        if (c == 1.0f && in == out) continue;
+        if (c * down == 1.0f && in == out) continue;
         with_type(b.type[tensor], [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
             Eight<T> v[kEights<T>];
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_clip_scale(const Batch b, const do
             for (int q = 0; q < kEights<T>; ++q) {
                 const int j = (q * kThreads + threadIdx.x) * 8;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[q].set(e, v[q].at(e) * c);
+                for (int e = 0; e < 8; ++e) v[q].set(e, v[q].at(e) * c * down);
                 v[q].store_through(y + j, p.count - j);
             }
         });

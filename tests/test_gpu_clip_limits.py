@@ -1,11 +1,13 @@
-"""Clipping at the ends: infinities and NaN beside every kind of limit."""
+"""Clipping at the ends: infinities and NaN beside every kind of limit, and
+factors that fp32 does not hold. Bounds: as test_gpu_clip.py, with one rounding
+more of the product (3 e relative beside the output's half ulp)."""
 
 import numpy as np
 import pytest
 import torch
 
 import int8_quantized_matmul_amd as i8
-from adapt_util import randn, wide
+from adapt_util import EPS32, near, randn, wide
 from gpu_util import say
 from oracle import adapt
 
@@ -38,3 +40,19 @@ def test_not_finite_gradients(bad, max_norm, in_place):
         assert np.array_equal(wide(t), r, equal_nan=True)
         if max_norm == INF:
             assert torch.equal(t, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size,max_norm", [(1e30, 1e-10), (1e36, 1e-10), (1e36, 1e-30), (1e30, 1e-38)])
+def test_factors_beyond_fp32(size, max_norm, dtype):
+    """max_norm / N below fp32's normal numbers, or below all of them: the
+    products are numbers that fp32 holds."""
+    rng = np.random.default_rng(4)
+    g = [randn(rng, 70, dtype, size), randn(rng, (31, 33), dtype, size)]
+    say(f"  launch: clip_grad_norm of values near {size} to {max_norm} {dtype}")
+    out = [torch.empty_like(t) for t in g]
+    i8.clip_grad_norm(g, max_norm, out=out)
+    torch.cuda.synchronize()
+    _, ref = adapt.clip_grad_norm([wide(t) for t in g], float(np.float32(max_norm)))
+    for o, r in zip(out, ref):
+        near(o, r, 3 * EPS32 * np.abs(r), "out")
