@@ -128,6 +128,10 @@ hipError_t launch_outlier_matmul(const uint16_t* X_O, int64_t ldo,
 hipError_t launch_calib_mfma_i8(const int8_t* codes, int64_t blocks, int64_t iters, int32_t* out,
                                 hipStream_t stream);
 
+// Threads that one dimension of a grid can have. What is beyond them does not
+// run, and the launch reports no error.
+constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;
+
 // Element types of the kernels around an adapted layer (the values of
 // i8mm_dtype).
 enum class Dtype { F16 = 0, BF16 = 1, F32 = 2 };

@@ -361,6 +361,14 @@ int row_threads(int64_t h, int nv) {
     return static_cast<int>(((eights + nv - 1) / nv + 63) / 64 * 64);
 }
 
+// Calls f(first, n) for the s rows in runs of n whose grid, a block of
+// `threads` for each `rows` of them, is one that can be launched.
+template <typename F>
+void for_rows(int64_t s, int rows, int threads, F&& f) {
+    const int64_t most = kGridThreads / threads * rows;
+    for (int64_t first = 0; first < s; first += most) f(first, s - first < most ? s - first : most);
+}
+
 }  // namespace
 
 hipError_t launch_layer_norm(const void* X, int64_t ldx, Dtype xt, int64_t s, int64_t h, const void* w, const void* b,
@@ -374,9 +382,12 @@ hipError_t launch_layer_norm(const void* X, int64_t ldx, Dtype xt, int64_t s, in
             constexpr int NV = decltype(nv)::value;
             const int threads = row_threads(h, NV);
             const int rows = threads >= 256 ? 1 : 256 / threads;      // rows of a block
-            k_layer_norm<T, W, NV><<<static_cast<unsigned>((s + rows - 1) / rows), threads * rows, 0, stream>>>(
-                static_cast<const T*>(X), ldx, s, static_cast<int>(h), threads, static_cast<const W*>(w),
-                static_cast<const W*>(b), eps, static_cast<T*>(Y), ldy, mean, rstd);
+            for_rows(s, rows, threads * rows, [&](int64_t first, int64_t n) {
+                k_layer_norm<T, W, NV><<<static_cast<unsigned>((n + rows - 1) / rows), threads * rows, 0, stream>>>(
+                    static_cast<const T*>(X) + first * ldx, ldx, n, static_cast<int>(h), threads,
+                    static_cast<const W*>(w), static_cast<const W*>(b), eps, static_cast<T*>(Y) + first * ldy, ldy,
+                    mean ? mean + first : nullptr, rstd ? rstd + first : nullptr);
+            });
         };
         // Few rows (fewer than two a CU): as many threads as a row takes, for
         // latency. Otherwise 64 bytes a thread, so that short rows need one
@@ -390,9 +401,12 @@ hipError_t launch_layer_norm(const void* X, int64_t ldx, Dtype xt, int64_t s, in
         else if (nv == 4) go(std::integral_constant<int, 4>());
         else if (nv == 8) go(std::integral_constant<int, 8>());
         else
-            k_layer_norm_long<T, W><<<static_cast<unsigned>(s), kMaxThreads, 0, stream>>>(
-                static_cast<const T*>(X), ldx, static_cast<int>(h), static_cast<const W*>(w),
-                static_cast<const W*>(b), eps, static_cast<T*>(Y), ldy, mean, rstd);
+            for_rows(s, 1, kMaxThreads, [&](int64_t first, int64_t n) {
+                k_layer_norm_long<T, W><<<static_cast<unsigned>(n), kMaxThreads, 0, stream>>>(
+                    static_cast<const T*>(X) + first * ldx, ldx, static_cast<int>(h), static_cast<const W*>(w),
+                    static_cast<const W*>(b), eps, static_cast<T*>(Y) + first * ldy, ldy,
+                    mean ? mean + first : nullptr, rstd ? rstd + first : nullptr);
+            });
         return hipGetLastError();
     });
 }
@@ -436,9 +450,12 @@ hipError_t launch_layer_norm_backward(const void* dY, int64_t lddy, const void* 
             } else if (row_threads(h, 4) <= 512) {
                 pick(integral_constant<int, 4>(), integral_constant<int, 512>());
             } else {
-                k_layer_norm_dx_long<T, W><<<static_cast<unsigned>(s), kMaxThreads, 0, stream>>>(
-                    static_cast<const T*>(dY), lddy, static_cast<const T*>(X), ldx, static_cast<int>(h),
-                    static_cast<const W*>(w), mean, rstd, static_cast<T*>(dX), lddx);
+                for_rows(s, 1, kMaxThreads, [&](int64_t first, int64_t n) {
+                    k_layer_norm_dx_long<T, W><<<static_cast<unsigned>(n), kMaxThreads, 0, stream>>>(
+                        static_cast<const T*>(dY) + first * lddy, lddy, static_cast<const T*>(X) + first * ldx, ldx,
+                        static_cast<int>(h), static_cast<const W*>(w), mean + first, rstd + first,
+                        static_cast<T*>(dX) + first * lddx, lddx);
+                });
                 const int64_t rows = (s + parts - 1) / parts;
                 if (params)
                     k_layer_norm_dw_long<T>
