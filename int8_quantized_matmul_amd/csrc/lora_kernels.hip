@@ -787,6 +787,7 @@ struct Plan {
     float* most;                     // [2 rank tiles][tiles][16]: each rank's largest finite |factor|
     int32_t* exps;                   // [slots][2 rank tiles][16]: the power of two of each chunk and rank
     int slots, tiles, rank_tiles;
+    unsigned first_block;            // of this launch among the blocks of grad
 };
 
 constexpr int kPlanThreads = 1024;
@@ -1021,8 +1022,9 @@ struct GradBlock {
     __device__ __forceinline__ GradBlock(const Side& x, const Side& y, int r, const Plan& plan) {
         const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
         const int xblocks = (x.len + 127) / 128, blocks = xblocks + (y.len + 127) / 128;
-        const int cb = blocks - 1 - static_cast<int>(blockIdx.x % blocks);
-        chunk = blockIdx.x / blocks;
+        const unsigned block = plan.first_block + blockIdx.x;
+        const int cb = blocks - 1 - static_cast<int>(block % blocks);
+        chunk = block / blocks;
         c = plan.chunks[chunk];
         second = cb >= xblocks;
         len = second ? y.len : x.len;
@@ -1087,8 +1089,9 @@ struct GradBlock {
 // the zeros of adapters that no token carries. True for such a block.
 __device__ __forceinline__ bool write_zeros(const Side& x, const Side& y, int r, const Plan& plan) {
     const int xblocks = (x.len + 127) / 128, blocks = xblocks + (y.len + 127) / 128;
-    if (blockIdx.x < static_cast<unsigned>(plan.slots) * blocks) return false;
-    const int at = blockIdx.x - plan.slots * blocks, g = at / blocks, cb = at % blocks;
+    const unsigned block = plan.first_block + blockIdx.x;
+    if (block < static_cast<unsigned>(plan.slots) * blocks) return false;
+    const int at = block - plan.slots * blocks, g = at / blocks, cb = at % blocks;
     if (plan.count[g] > 0) return true;
     const bool second = cb >= xblocks;
     const int len = second ? y.len : x.len, col = (second ? cb - xblocks : cb) * 128 + (threadIdx.x & 31) * 4;
@@ -1425,9 +1428,8 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const int rt = static_cast<int>(up(a.r, 16));
-    const Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
-                    reinterpret_cast<Chunk*>(ws + l.chunks), floats(l.most), ints(l.exps), l.slots,
-                    l.tiles, rt};
+    Plan plan{ints(l.order), ints(l.count), ints(l.part), ints(l.tile_chunk),
+              reinterpret_cast<Chunk*>(ws + l.chunks), floats(l.most), ints(l.exps), l.slots, l.tiles, rt, 0};
     float* dT = floats(l.dT);
     const Side x{X, ldx, static_cast<int>(a.h), dT, ws + l.laid[0], dA, floats(l.sums[0])};
     const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
@@ -1451,12 +1453,16 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
         k_lora_lay<T><<<per_tile, kThreads, 0, stream>>>(x, y, a.scale, r, plan);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         // without partial sums the same launch also writes the zeros
-        const unsigned blocks =
-            static_cast<unsigned>((l.slots + (l.KC < a.s ? 0 : a.G)) * (up(a.h, 128) + up(a.o, 128)));
-        if (rt == 1) k_lora_grad<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
-        else if (rt == 2) k_lora_grad<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
-        else if (rt <= 4) k_lora_grad_shared<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
-        else k_lora_grad_shared<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+        const int64_t all = (l.slots + (l.KC < a.s ? 0 : a.G)) * (up(a.h, 128) + up(a.o, 128));
+        // tens of thousands of adapters on wide layers are more than one grid holds
+        for (int64_t first = 0, most = kGridThreads / kThreads; first < all; first += most) {
+            plan.first_block = static_cast<unsigned>(first);
+            const unsigned blocks = static_cast<unsigned>(all - first < most ? all - first : most);
+            if (rt == 1) k_lora_grad<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+            else if (rt == 2) k_lora_grad<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+            else if (rt <= 4) k_lora_grad_shared<T, 1><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+            else k_lora_grad_shared<T, 2><<<blocks, kThreads, 0, stream>>>(x, y, r, plan);
+        }
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (dX && (e = add_many<T>(a, ws + l.d.parts, ints(l.d.exps), a.A, a.h, base, ldb, dX, lddx, stream)) !=
                       hipSuccess)
