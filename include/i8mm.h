@@ -605,7 +605,8 @@ size_t i8mm_lora_forward_workspace_bytes(int64_t s, int64_t h, int64_t o, int64_
  * i8mm_lora_forward_workspace_bytes(s, h, o, r) bytes, 256-byte aligned,
  * contents unspecified before and after.
  * Values of another row, or of an adapter that a row does not carry, never
- * reach it, NaN and infinity included.
+ * reach it, NaN and infinity included. Infinities among the inputs and the
+ * adapters give the infinities and NaN that the formulas give.
  */
 i8mm_status i8mm_lora_forward(const void* X, int64_t ldx, const void* A, const void* B, int32_t type,
                               int64_t n_adapters, int64_t r, const int32_t* ids, const float* scale,

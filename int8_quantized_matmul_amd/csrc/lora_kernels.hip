@@ -103,16 +103,47 @@ __device__ __forceinline__ float finite_size(float v) {
 }
 
 // v 2^ex as a sum of N parts of type T. What is not finite is its own first
-// part.
+// part; what T rounds to 0 is a first part of T's smallest number less as much
+// in the second, so that a first part is 0 for 0 alone.
 template <typename T, int N>
 __device__ __forceinline__ void split(float v, int ex, T(&part)[N]) {
+    const float whole = v;
     if constexpr (kScaled<T>) v = ldexpf(v, ex);
     const bool finite = fabsf(v) < __builtin_inff();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         part[k] = from_float<T>(v);
+        if (k == 0 && to_float<T>(part[0]) == 0.0f && whole != 0.0f)
+            part[0] = __builtin_bit_cast(T, static_cast<uint16_t>(whole < 0.0f ? 0x8001 : 1));
         v = finite ? v - to_float<T>(part[k]) : 0.0f;
     }
+}
+
+// An infinity times a factor's first part is what the definition gives. Its
+// products with the other parts, of either sign or 0, are not: they would make
+// NaN of it. Sums are formed without regard to that first; if there is a NaN
+// among them, they are formed again, and there the other parts meet 0 in the
+// place of what is not finite.
+template <typename T>
+__device__ __forceinline__ Vec<T> finite_only(const Vec<T>& v) {
+    constexpr unsigned kExponent = kScaled<T> ? 0x7c00u : 0x7f80u;
+    v4u w = __builtin_bit_cast(v4u, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if ((w[k] & kExponent) == kExponent) w[k] &= 0xffff0000u;
+        if ((w[k] & kExponent << 16) == kExponent << 16) w[k] &= 0xffffu;
+    }
+    return __builtin_bit_cast(Vec<T>, w);
+}
+
+// Whether a lane of the wavefront may have a NaN among its sums (infinities of
+// both signs count too).
+template <int N>
+__device__ __forceinline__ bool any_nan(const v4f (&sum)[N]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) t += (sum[k][0] + sum[k][1]) + (sum[k][2] + sum[k][3]);
+    return __ballot(t != t) != 0;
 }
 
 // Few tokens (at most kFew): a block takes one adapter and finds its tokens
@@ -565,6 +596,7 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
             to[2 * 16 * 8] = part[1];
         }
         __syncthreads();
+        unsigned again = 0;
         v4f sum[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -580,9 +612,39 @@ __global__ __launch_bounds__(kThreads, 3) void k_lora_add_few(const float* __res
         for (int e = 0; e < 4; ++e) {
             const float factor = factor_of(f, exps[q * 4 + e]);
             Vec<T> y;
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(sum[j][e], factor, to_float<T>(b[e][j])));
-            if (at[e] >= 0) *reinterpret_cast<Vec<T>*>(out + static_cast<int64_t>(at[e]) * ldo + col) = y;
+            for (int j = 0; j < 8; ++j) {
+                v[j] = fmaf(sum[j][e], factor, to_float<T>(b[e][j]));
+                y[j] = from_float<T>(v[j]);
+            }
+            const float all = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            const bool nan = all != all;             // or infinities of both signs
+            if (at[e] >= 0 && !nan) *reinterpret_cast<Vec<T>*>(out + static_cast<int64_t>(at[e]) * ldo + col) = y;
+            again |= (at[e] >= 0 && nan) << e;
+        }
+        // What has a NaN is formed again with care, without the matrix instruction:
+        // kept apart from the sums above, it costs them no registers.
+        while (again) {
+            const int t = q * 4 + __builtin_ctz(again);
+            again &= again - 1;
+            v8f whole = {};
+#pragma unroll 1
+            for (int k = 0; k < r; ++k) {
+                const T* part = parts + ((k / 16 * 4 + k / 8 % 2) * 16 + t) * 8 + k % 8;
+                const float hi = to_float<T>(part[0]), lo = to_float<T>(part[2 * 16 * 8]);
+                const Vec<T> m = load16(Mg + static_cast<int64_t>(k) * len + mcol), others = finite_only<T>(m);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    whole[j] = fmaf(lo, to_float<T>(others[j]), fmaf(hi, to_float<T>(m[j]), whole[j]));
+            }
+            const int64_t i = tokens[first + t];
+            const Vec<T> old = base ? load16(base + i * ldb + col) : Vec<T>{};
+            const float factor = factor_of(f, exps[t]);
+            Vec<T> y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = from_float<T>(fmaf(whole[j], factor, to_float<T>(old[j])));
+            *reinterpret_cast<Vec<T>*>(out + i * ldo + col) = y;
         }
     }
 }
@@ -756,6 +818,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_add_many(const T* __restri
                     load_ranks<T>(Mg, len, r, st, q, mcol, columns[0]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] = mma(p, columns[0][j], sum[j]);
+                }
+            }
+            if (any_nan(sum)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                const auto careful = [&](const Vec<T>& p, auto&& column) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)          // lanes of q >= 2 hold what the second parts meet
+                        sum[j] = mma(p, q >= 2 ? finite_only<T>(column(j)) : column(j), sum[j]);
+                };
+                if constexpr (ST > 0) {
+#pragma unroll
+                    for (int st = 0; st < ST; ++st)
+                        careful(now.p[st], [&](int j) { return LDS ? mine[(st * 8 + j) * 32] : columns[LDS ? 0 : st][j]; });
+                } else {
+                    for (int st = 0; st < steps; ++st) {
+                        const Vec<T> p = load16(parts + ((static_cast<int64_t>(tile) * steps + st) * 64 + lane) * 8);
+                        load_ranks<T>(Mg, len, r, st, q, mcol, columns[0]);
+                        careful(p, [&](int j) { return columns[0][j]; });
+                    }
                 }
             }
             float factor[4];
@@ -1085,6 +1167,36 @@ struct GradBlock {
     }
 };
 
+// The sums of RT tiles of ranks over the whole chunk by one wavefront, with
+// care for infinities in Z: only for chunks that have made a NaN.
+template <typename T, int RT>
+__device__ __forceinline__ void careful_sums(const GradBlock<T>& b, const Plan& plan, int rt, v4f(&sum)[RT][8]) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int st = 0; st < b.steps; ++st) {
+        Vec<T> rows[8], columns[8];
+        b.rows_of(st, b.tokens_of(st), rows);
+        transpose8<T>(rows, columns);
+#pragma unroll
+        for (int p = 0; p < kParts<T>; ++p) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                Vec<T> f[kParts<T>];
+                b.factors_of(plan, st, rt + t < plan.rank_tiles ? rt + t : plan.rank_tiles - 1, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[t][j] = mma(f[p], columns[j], sum[t][j]);
+            }
+            if (p == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) columns[j] = finite_only<T>(columns[j]);
+            }
+        }
+    }
+}
+
 // Blocks past those of the chunks, one for each adapter and 128 columns, write
 // the zeros of adapters that no token carries. True for such a block.
 __device__ __forceinline__ bool write_zeros(const Side& x, const Side& y, int r, const Plan& plan) {
@@ -1156,6 +1268,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r
         }
     }
     if (wave != 0) return;
+    bool nan = false;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) nan |= any_nan(sum[t]);
+    if (nan) careful_sums<T, RT>(b, plan, 0, sum);
 #pragma unroll
     for (int t = 0; t < RT; ++t) b.store(plan, t, r, sum[t]);
 }
@@ -1215,6 +1331,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_lora_grad_shared(Side x, Side y
             }
         }
     }
+    bool nan = false;
+#pragma unroll
+    for (int t = 0; t < RW; ++t) nan |= any_nan(sum[t]);
+    if (nan) careful_sums<T, RW>(b, plan, wave * RW, sum);
 #pragma unroll
     for (int t = 0; t < RW; ++t)
         if (wave * RW + t < plan.rank_tiles) b.store(plan, wave * RW + t, r, sum[t]);
