@@ -1389,9 +1389,16 @@ int dot_splits(int64_t s, int64_t len, int64_t r) {
 // Parts for a tile's later adapters, where a pass takes one adapter. 4096 x
 // 36864, rank 64, one tile with two adapters: 115 us with as many parts as the
 // first has, 95 with 16, 89 with 32, 83 without such a tile; rank 128, four
-// such tiles: 223, 174, 164.
-int dot_late(int splits, int64_t r) {
-    const int n = 8 * splits < 32 ? 8 * splits : 32;
+// such tiles: 223, 174, 164. Every token has room for as many sums, so they
+// become fewer as the tiles become more: what the launch waits for at its end,
+// a part of a later adapter, is then a smaller share of it anyway (rank 64, 12288
+// columns, 131072 tokens: 749 us with 8 parts, 733 with 4; 262144: 1472 with 8,
+// 1421 with 2; but 65536 tokens, 36864 columns: 1030 with 8, 1153 with 1), and the
+// room beyond one sum a token stays below 135 MB.
+int dot_late(int64_t s, int splits, int64_t r) {
+    const int64_t room = 8192 / up(s > 0 ? s : 1, dot_tokens(static_cast<int>(r)));
+    int n = 8 * splits < 32 ? 8 * splits : 32;
+    if (room < n) n = static_cast<int>(room);
     return r <= 32 || splits > n ? splits : n;
 }
 
@@ -1400,7 +1407,7 @@ hipError_t dot(const LoraArgs& a, const void* Zv, int64_t ldz, const void* Mv, i
                hipStream_t stream) {
     const T* Z = static_cast<const T*>(Zv);
     const T* M = static_cast<const T*>(Mv);
-    const int splits = dot_splits(a.s, len, a.r), late = dot_late(splits, a.r), n = static_cast<int>(len);
+    const int splits = dot_splits(a.s, len, a.r), late = dot_late(a.s, splits, a.r), n = static_cast<int>(len);
     using std::integral_constant;
     const integral_constant<int, 1> one;
     const integral_constant<int, 2> two;
@@ -1468,7 +1475,7 @@ struct DotPlaces {
     size_t P, parts, exps;
     DotPlaces(Places& w, int64_t s, int64_t len, int64_t r) {
         const int splits = dot_splits(s, len, r);
-        P = w.take(4 * (few(s) ? splits : dot_late(splits, r)) * s * r);
+        P = w.take(4 * (few(s) ? splits : dot_late(s, splits, r)) * s * r);
         parts = w.take(up(s, 16) * up(r, 16) * 16 * 32 * 2);
         exps = w.take(4 * up(s, 16) * 16);
     }
@@ -1478,7 +1485,7 @@ template <typename T>
 hipError_t join(const LoraArgs& a, int splits, const float* P, float* Tout, void* parts, int32_t* exps,
                 hipStream_t stream) {
     k_lora_join<T><<<static_cast<unsigned>(up(a.s, 16)), kThreads, 0, stream>>>(
-        P, a.ids, a.G, splits, dot_late(splits, a.r), a.r, a.s, Tout, static_cast<T*>(parts), exps);
+        P, a.ids, a.G, splits, dot_late(a.s, splits, a.r), a.r, a.s, Tout, static_cast<T*>(parts), exps);
     return hipGetLastError();
 }
 
@@ -1555,7 +1562,7 @@ hipError_t backward(const LoraArgs& a, const void* dY, int64_t lddy, const void*
     const Side y{dY, lddy, static_cast<int>(a.o), Tp, ws + l.laid[1], dB, floats(l.sums[1])};
     const int r = a.r;
     float* P = floats(l.d.P);
-    const int splits = dot_splits(a.s, a.o, a.r), late = few(a.s) ? splits : dot_late(splits, a.r);
+    const int splits = dot_splits(a.s, a.o, a.r), late = few(a.s) ? splits : dot_late(a.s, splits, a.r);
     const auto plan_join = [&] {
         k_lora_plan_join<T>
             <<<static_cast<unsigned>(a.G + up(a.s, kPlanThreads / 16)), kPlanThreads, 0, stream>>>(
