@@ -1542,16 +1542,19 @@ __global__ __launch_bounds__(256) void k_outlier_only(const uint16_t* __restrict
                                                       float* __restrict__ C_O) {
     const int t = threadIdx.x, lane = t & 63, wid = t >> 6;
     const int64_t n_to = o / 16;
-    const int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + wid;
     const int64_t n_ts = (s + 15) / 16;
-    if (tile >= n_to * n_ts) return;
-    const int64_t to_i = tile % n_to, ts_i = tile / n_to;
     const int r16 = lane & 15, g = lane >> 4;
-    const int64_t srow = ts_i * 16 + r16;
-    v4f f = {0.f, 0.f, 0.f, 0.f};
-    f = outlier_tile_16x16(f, lane, to_i * 16, ts_i * 16, s, o, X_O, ldo, idx, n_out[0], W, nullptr, nullptr, nullptr);
-    const int64_t ocol = to_i * 16 + 4 * g;
-    if (srow < s) *reinterpret_cast<v4f*>(C_O + srow * o + ocol) = f;
+    // one tile a wavefront, more if they are more than a grid holds
+    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + wid; tile < n_to * n_ts;
+         tile += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t to_i = tile % n_to, ts_i = tile / n_to;
+        const int64_t srow = ts_i * 16 + r16;
+        v4f f = {0.f, 0.f, 0.f, 0.f};
+        f = outlier_tile_16x16(f, lane, to_i * 16, ts_i * 16, s, o, X_O, ldo, idx, n_out[0], W, nullptr, nullptr,
+                               nullptr);
+        const int64_t ocol = to_i * 16 + 4 * g;
+        if (srow < s) *reinterpret_cast<v4f*>(C_O + srow * o + ocol) = f;
+    }
 }
 
 // Weight tiles per group of the grouped tile order (grouped_tile): 4 when
@@ -1705,8 +1708,9 @@ hipError_t launch_decode_fused(const uint16_t* X, int64_t s, int64_t h, int64_t 
 
 hipError_t launch_outlier_matmul(const uint16_t* X_O, int64_t ldo, const int32_t* idx, const int32_t* n_out,
                                  const uint16_t* W, int64_t s, int64_t o, float* C_O, hipStream_t stream) {
-    const int64_t tiles = (o / 16) * ((s + 15) / 16);
-    hipLaunchKernelGGL(k_outlier_only, dim3(static_cast<unsigned>((tiles + 3) / 4)), dim3(256), 0, stream,
+    const int64_t tiles = (o / 16) * ((s + 15) / 16), most = kGridThreads / 256;
+    const int64_t blocks = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
+    hipLaunchKernelGGL(k_outlier_only, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
                        X_O, ldo, idx, n_out, W, s, o, C_O);
     return hipGetLastError();
 }

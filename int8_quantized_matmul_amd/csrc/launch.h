@@ -8,6 +8,24 @@
 
 namespace i8mm {
 
+// Threads that one dimension of a grid can have. What is beyond them does not
+// run, and the launch reports no error.
+constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;
+
+// Rows of the int8 path's row kernels that one launch takes, at a block of 256
+// threads a row or less; more go in runs.
+constexpr int64_t kRowsAtOnce = int64_t(1) << 23;
+
+// Calls f(first, n) for s rows in runs of at most `most`, until one fails.
+template <typename F>
+hipError_t for_row_runs(int64_t s, int64_t most, F&& f) {
+    for (int64_t first = 0; first < s; first += most) {
+        const hipError_t e = f(first, s - first < most ? s - first : most);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch_detect(const uint16_t* X, int64_t s, int64_t h, float alpha,
                          uint32_t* mask, int32_t* idx, int32_t* n_out, hipStream_t stream);
 
@@ -127,10 +145,6 @@ hipError_t launch_outlier_matmul(const uint16_t* X_O, int64_t ldo,
 // thread, out one int32 per thread.
 hipError_t launch_calib_mfma_i8(const int8_t* codes, int64_t blocks, int64_t iters, int32_t* out,
                                 hipStream_t stream);
-
-// Threads that one dimension of a grid can have. What is beyond them does not
-// run, and the launch reports no error.
-constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;
 
 // Element types of the kernels around an adapted layer (the values of
 // i8mm_dtype).

@@ -739,15 +739,24 @@ namespace {
 hipError_t launch_detect_into(const uint16_t* X, int64_t s, int64_t h, float alpha, uint32_t* mask,
                               hipStream_t stream) {
     const int64_t n_strips = (h + 511) / 512;
-    const int64_t blocks = n_strips * ((s + kDetRows - 1) / kDetRows);
-    hipLaunchKernelGGL(k_detect, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
-                       X, s, h, make_threshold(alpha), n_strips, mask);
-    return hipGetLastError();
+    return for_row_runs(s, kGridThreads / 256 / n_strips * kDetRows, [&](int64_t first, int64_t n) {
+        const int64_t blocks = n_strips * ((n + kDetRows - 1) / kDetRows);
+        hipLaunchKernelGGL(k_detect, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                           X + first * h, n, h, make_threshold(alpha), n_strips, mask);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_rows(const uint16_t* X, int64_t s, int64_t h, const uint32_t* src_mask, uint32_t* mask_out,
                        int32_t* idx, int32_t* n_out, int8_t* Xq, float* c_x, uint16_t* X_O, int64_t ldo,
                        hipStream_t stream) {
+    if (s > kRowsAtOnce)
+        return for_row_runs(s, kRowsAtOnce, [&](int64_t first, int64_t n) {
+            const bool one = first == 0;     // the first run writes the outlier set
+            return launch_rows(X + first * h, n, h, src_mask, one ? mask_out : nullptr, one ? idx : nullptr,
+                               one ? n_out : nullptr, Xq ? Xq + first * h : nullptr, c_x + first, X_O + first * ldo,
+                               ldo, stream);
+        });
     // Wavefronts per row: enough for ~4096 wavefronts in all (4 per SIMD),
     // and more while a lane would hold over 8 chunks of its row (long rows:
     // at 4096 x 12288 four wavefronts per row took the prologue from 54 to
@@ -929,13 +938,21 @@ hipError_t launch_quantize_tensorwise(const uint16_t* X, int64_t s, int64_t h, c
 #undef I8MM_TW
         return hipGetLastError();
     }
-    const dim3 grid(static_cast<unsigned>((s + 3) / 4)), block(256);
-    hipLaunchKernelGGL((k_quant_rows<0, RowScale::MaxOnly>), grid, block, dyn, stream, X, s, h, mask, mask_out,
-                       idx, n_out, Xq, c_x, X_O, ldo);
+    hipError_t e = for_row_runs(s, kRowsAtOnce, [&](int64_t first, int64_t n) {
+        const bool one = first == 0;         // the first run writes the outlier set
+        hipLaunchKernelGGL((k_quant_rows<0, RowScale::MaxOnly>), dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256),
+                           dyn, stream, X + first * h, n, h, mask, one ? mask_out : nullptr, one ? idx : nullptr,
+                           one ? n_out : nullptr, Xq + first * h, c_x + first, X_O + first * ldo, ldo);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_tensor_scale, dim3(1), dim3(1024), 0, stream, c_x, s);
-    hipLaunchKernelGGL((k_quant_rows<0, RowScale::Given>), grid, block, dyn, stream, X, s, h, mask, nullptr,
-                       nullptr, nullptr, Xq, c_x, X_O, ldo);
-    return hipGetLastError();
+    return for_row_runs(s, kRowsAtOnce, [&](int64_t first, int64_t n) {
+        hipLaunchKernelGGL((k_quant_rows<0, RowScale::Given>), dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256),
+                           dyn, stream, X + first * h, n, h, mask, nullptr, nullptr, nullptr, Xq + first * h,
+                           c_x + first, X_O + first * ldo, ldo);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_quantize_weights_tensorwise(const uint16_t* W, int64_t h, int64_t o, int8_t* Wq, float* c_w,

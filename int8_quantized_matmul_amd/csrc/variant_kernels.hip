@@ -352,6 +352,13 @@ __global__ __launch_bounds__(256) void k_quant_cols_zp(const uint16_t* __restric
 hipError_t launch_quantize_rows_zp(const uint16_t* X, int64_t s, int64_t h, const uint32_t* mask, int8_t* Xq,
                                    float* nd_x, int32_t* zp_x, int32_t* rowsum_x, uint16_t* X_O, int64_t ldo,
                                    hipStream_t stream, uint32_t* mask_out, int32_t* idx, int32_t* n_out) {
+    if (s > kRowsAtOnce)
+        return for_row_runs(s, kRowsAtOnce, [&](int64_t first, int64_t n) {
+            const bool one = first == 0;     // the first run writes the outlier set
+            return launch_quantize_rows_zp(X + first * h, n, h, mask, Xq + first * h, nd_x + first, zp_x + first,
+                                           rowsum_x + first, X_O + first * ldo, ldo, stream, one ? mask_out : nullptr,
+                                           one ? idx : nullptr, one ? n_out : nullptr);
+        });
     const size_t dyn = static_cast<size_t>(2 * (h / 32) * 4);
     // Wavefronts per row as for the absmax row quantiser: ~4096 wavefronts
     // in all while each holds at most 16 chunks of its row.
