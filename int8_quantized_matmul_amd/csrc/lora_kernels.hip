@@ -217,10 +217,11 @@ struct Adapters {
 // second pass. Where the registers hold one (NA = 1), slot 0 takes the tile's
 // first adapter and the others the rest, in `late` parts instead of `splits`:
 // they are few, and as long as slot 0's they would be what the launch waits
-// for. Bound by memory up to 32 ranks (4096 x 12288, rank 16: 24-30 us,
-// 3.4-4.2 TB/s, 20 for one adapter) and by the CU's loads beyond, where M's
-// pieces are as many as Z's (4096 x 36864, rank 64: 69 us for one adapter, 4.4
-// TB/s). The next step's loads go before this one's sums (78 us without).
+// for. Bound by memory up to 32 ranks (4096 x 12288, rank 16: 20 us by itself,
+// 5.0 TB/s, 24-34 after an add, whose results are still being written back) and
+// by the CU's loads beyond, where M's pieces are as many as Z's (4096 x 36864,
+// rank 64, one adapter: 65-69 us by itself, 4.4 TB/s, 81 after an add). The next
+// step's loads go before this one's sums (78 us by itself without).
 __host__ __device__ constexpr int dot_tokens(int r) { return r > 64 ? 32 : 64; }
 
 template <typename T, int MT, int RT, int NA>
@@ -1216,8 +1217,8 @@ __device__ __forceinline__ bool write_zeros(const Side& x, const Side& y, int r,
 // Up to 32 ranks (RT tiles): every wavefront takes all ranks and every fourth
 // tile, with the next one's rows, and the tokens of the one after, on their
 // way while this one's sums are formed; the four sums are joined in LDS. Bound
-// by memory: 4096 tokens x (12288 + 36864), 403 MB: rank 16 75 us (5.4 TB/s),
-// rank 32 85 us.
+// by memory: 4096 tokens x (12288 + 36864), 403 MB: rank 16 74-77 us (5.3 TB/s),
+// rank 32 86-89 us.
 template <typename T, int RT>
 __global__ __launch_bounds__(kThreads, 2) void k_lora_grad(Side x, Side y, int r, Plan plan) {
     __shared__ v4f join[2][RT * 8][64];
@@ -1367,8 +1368,11 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // for each adapter. With many, a block takes a tile of neighbours, most of
 // which have one adapter; where a pass does not take two of them, the others
 // have blocks of their own, which leave at once in all other tiles (4096 x
-// 36864, rank 64, two adapters that meet inside a tile: 145 us for the one
-// block's two passes, 115 for two blocks, 89 with the second in smaller parts).
+// 36864, rank 64, two adapters that meet inside a tile, in a backward pass: 145 us
+// for the one block's two passes, 115 for two blocks, 90 with the second in
+// smaller parts). Tokens of many adapters in turn cost their tiles a pass for
+// each: 512 tokens of 64 adapters, 12288 -> 36864, rank 16: dot 50 and add 88 us,
+// 19 and 35 for the same tokens in the adapters' order.
 bool few(int64_t s) { return s <= kFew; }
 int tile_slots(int64_t s, int64_t r) { return s <= 1024 ? 4 : r > 32 ? 2 : 1; }
 int few_slots(int64_t s, int64_t G) { return static_cast<int>(G < s ? G : s); }
@@ -1377,8 +1381,8 @@ int few_spread(int64_t s) { return static_cast<int>(up(s, 64)); }
 
 // Parts that dot splits len into; each wavefront keeps at least two steps of
 // 64. Few tokens: 8 to 16, so that one adapter alone has blocks enough. Many:
-// about one block a CU (4096 x 36864, rank 64: 69 us at 256 blocks, 78 at 512,
-// 87 at 1024).
+// about one block a CU (4096 x 36864, rank 64, by itself: 69 us at 256 blocks, 78
+// at 512, 87 at 1024).
 int dot_splits(int64_t s, int64_t len, int64_t r) {
     const int64_t most = len / 64 / 8;
     const int64_t want = few(s) ? (s <= 16 ? 16 : 8) : up(kCus, up(s, dot_tokens(static_cast<int>(r))));
@@ -1387,9 +1391,9 @@ int dot_splits(int64_t s, int64_t len, int64_t r) {
 }
 
 // Parts for a tile's later adapters, where a pass takes one adapter. 4096 x
-// 36864, rank 64, one tile with two adapters: 115 us with as many parts as the
-// first has, 95 with 16, 89 with 32, 83 without such a tile; rank 128, four
-// such tiles: 223, 174, 164. Every token has room for as many sums, so they
+// 36864, rank 64, one tile with two adapters, in a backward pass: 115 us with as
+// many parts as the first has, 95 with 16, 90 with 32, 83 without such a tile;
+// rank 128, four such tiles, by itself: 223, 174, 162. Every token has room for as many sums, so they
 // become fewer as the tiles become more: what the launch waits for at its end,
 // a part of a later adapter, is then a smaller share of it anyway (rank 64, 12288
 // columns, 131072 tokens: 749 us with 8 parts, 733 with 4; 262144: 1472 with 8,

@@ -58,8 +58,8 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, v2f* red, int waves
 // read of X and the single write of Y (NV groups of eight elements a thread).
 // The variance is taken about the mean, from the registers. Bound by memory:
 // 4096 x 12288 of fp16 takes 38-42 us, 4.8-5.2 TB/s of the bytes it has to
-// move, where a large copy on this card reaches 4.9-5.1; 8 x 12288 takes 4 us,
-// two trips to memory and a launch.
+// move, where a large copy on this card reaches 4.9-5.1; 8 x 12288 takes 4.4-4.9
+// us, two trips to memory and a launch.
 template <typename T, typename W, int NV>
 __global__ __launch_bounds__(kMaxThreads) void k_layer_norm(const T* X, int64_t ldx, int64_t s, int h, int tw,
                                                             const W* __restrict__ w, const W* __restrict__ b,
@@ -272,7 +272,8 @@ __global__ __launch_bounds__(MAXT) void k_layer_norm_grad(const T* __restrict__ 
 }
 
 // Rows that the registers do not hold: dX by one block a row, reading it
-// twice, and the column sums by a second pass over both inputs.
+// twice, and the column sums by a second pass over both inputs. 4096 x 20480 of
+// fp16: 179 and 106 us, where one pass at a copy's rate would take 101.
 template <typename T, typename W>
 __global__ __launch_bounds__(kMaxThreads) void k_layer_norm_dx_long(const T* __restrict__ dY, int64_t lddy,
                                                                     const T* __restrict__ X, int64_t ldx, int h,
@@ -392,8 +393,8 @@ hipError_t launch_layer_norm(const void* X, int64_t ldx, Dtype xt, int64_t s, in
         // Few rows (fewer than two a CU): as many threads as a row takes, for
         // latency. Otherwise 64 bytes a thread, so that short rows need one
         // wavefront and no barrier, and long ones keep several blocks a CU.
-        // Measured, s x h of fp16: 8 x 12288 3.9 us at 16 or 32 bytes a
-        // thread, 4.7 at 64; 4096 x 12288 42.4 at 32, 38.0 at 64, 40.2 at 128.
+        // Measured, s x h of fp16: 8 x 12288 0.8 us more at 64 bytes a thread
+        // than at 16 or 32; 4096 x 12288 42.4 at 32, 38.0 at 64, 40.2 at 128.
         int nv = s < 2 * kCus ? 1 : static_cast<int>(64 / (8 * sizeof(T)));
         while (nv <= 8 && row_threads(h, nv) > kMaxThreads) nv *= 2;
         if (nv == 1) go(std::integral_constant<int, 1>());
@@ -442,7 +443,9 @@ hipError_t launch_layer_norm_backward(const void* dY, int64_t lddy, const void* 
             };
             using std::integral_constant;
             // The fewest columns a thread whose row fits a block; each NV with the most
-            // threads whose registers hold its sums, g, n and the row in flight.
+            // threads whose registers hold its sums, g, n and the row in flight. fp32
+            // rows beyond 12288 columns spill at that (4096 x 16384: 212 us for 805 MB,
+            // 3.8 TB/s; fp16 83 us, 4.8 TB/s).
             if (row_threads(h, 1) <= 512) {
                 pick(integral_constant<int, 1>(), integral_constant<int, 1024>());
             } else if (row_threads(h, 2) <= 768) {
