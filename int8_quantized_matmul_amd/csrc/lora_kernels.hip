@@ -113,6 +113,8 @@ __device__ __forceinline__ void split(float v, int ex, T(&part)[N]) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         part[k] = from_float<T>(v);
+        if (!kScaled<T> && k == 0 && finite)             // not rounded up to infinity
+            part[0] = from_float<T>(fminf(fmaxf(v, -0x1.fep127f), 0x1.fep127f));
         if (k == 0 && to_float<T>(part[0]) == 0.0f && whole != 0.0f)
             part[0] = __builtin_bit_cast(T, static_cast<uint16_t>(whole < 0.0f ? 0x8001 : 1));
         v = finite ? v - to_float<T>(part[k]) : 0.0f;

@@ -70,3 +70,31 @@ def test_a_rank_that_is_not_finite_leaves_the_others(s, h, o, r, G, kind, bad, d
     bb = ((link + 2.0 ** -22) * ft + 2.0 ** -20 * ft.max(axis=0)).T @ np.abs(dy)
     near(dB[0][torch.from_numpy(keep)], rb[0], bb, "dB of the finite ranks")
     assert not torch.isfinite(dA[0, r // 2]).all() and not torch.isfinite(dB[0, r // 2]).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_factors_at_the_end_of_fp32(dtype):
+    """T between bf16's largest number and fp32's, in dB and, from a product
+    that is as large, in Y."""
+    c = _case(40, 128, 192, 4, 1, "one", dtype, seed=10)
+    top = float(np.finfo(np.float32).max)
+    c["scale"].fill_(1.0)
+    T = torch.randn((40, 4), generator=torch.Generator().manual_seed(1)).to(c["X"].device)
+    T[7, 1], T[9, 2] = top, -0.999 * top
+    c["dY"] = (c["dY"] * 2.0 ** -4).to(dtype)
+    say(f"  launch: lora with factors at the end of fp32 {dtype}")
+    _, _, dB = i8.lora_backward(c["dY"], c["X"], T, c["A"], c["B"], c["ids"], c["scale"])
+    t, dy = wide(T), wide(c["dY"])
+    near(dB[0], t.T @ dy, ((_links(40) + 2.0 ** -20) * np.abs(t)).T @ np.abs(dy) + 2.0 ** -20 * np.abs(t).max(axis=0)[:, None]
+         * np.abs(dy).sum(axis=0), "dB")
+    if dtype == F16:
+        return
+    # X A = 255/256 2^128 from two factors of 2^64 and less, B small enough for Y
+    c["X"].zero_(), c["A"].zero_(), c["base"].zero_()
+    c["X"][:, 3], c["A"][0, :, 3] = 2.0 ** 64, 255 / 256 * 2.0 ** 64
+    c["X"][:, 4], c["A"][0, :, 4] = 2.0 ** 56, 0.75 * 2.0 ** 64
+    c["B"] = (c["B"] * 2.0 ** -120).to(dtype)
+    Y, T = i8.lora_forward(c["X"], c["A"], c["B"], c["ids"], c["scale"])
+    t, B = wide(T), wide(c["B"])[0]
+    assert np.isfinite(t).all() and np.abs(t).max() > 255.5 * 2.0 ** 120
+    near(Y, t @ B, 2.0 ** -14 * (np.abs(t) @ np.abs(B)), "Y")
