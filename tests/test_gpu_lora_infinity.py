@@ -2,7 +2,7 @@
 do the kernels, of the same sign; NaN where it gives NaN; and what it gives as
 finite is within 2^-8 of the largest finite value (test_gpu_lora.py has the
 tight bounds). The definition is taken in 64 bits from the kernels' own T, so
-that each product is judged by itself.
+that each product is compared by itself.
 """
 
 import numpy as np
