@@ -662,6 +662,178 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
                                 const int32_t* types, int64_t n, float max_norm, void* workspace,
                                 float* total_norm, hipStream_t stream);
 
+/*
+ * Decoding between int8 layers: a paged key-value cache, the attention of new
+ * tokens over it, and beam search.
+ *
+ * The pages of the method leave attention in 16 bits between the int8
+ * projections ([DIGEST] "Mixed-Precision Decomposition", memory accounting);
+ * these calls take that part of a decoding step: the fused projection's rows
+ * give queries, keys and values, the logits give the next tokens. The
+ * conventions of the calls around an adapted layer hold (row strides, element
+ * types, n = 0 or s = 0 accepted), and these:
+ *   - Keys and values lie in pools of pages, [n_pages][kv_heads][page][d] of
+ *     `type`, with a stride between pages (k_stride, v_stride, in elements,
+ *     a multiple of 8 and at least kv_heads page d). page is a multiple of 16.
+ *   - tables [n, max_pages] int32 (row stride ldt) names each sequence's pages
+ *     in order: position t of sequence i is slot t % page of page
+ *     tables[i][t / page]. One table serves all layers that share page numbers.
+ *   - lens [n] int32: each sequence's tokens. A length below 0 counts as 0, one
+ *     above max_pages * page as that; entries of a table's row beyond
+ *     ceil(len / page) are not read.
+ *   - A page number outside [0, n_pages) names no page: nothing is read from it
+ *     or written to it, and its positions are left out.
+ *   - refs [n_pages] int32: how many table entries (and whatever else a caller
+ *     counts in) hold each page. A page is free if its count is 0 or less.
+ */
+/* Limits: pages of a pool, tokens of a page, pages of a sequence (and max_pages
+ * * page < 2^31 - 4096), sequences of a call, features of a head (a multiple of
+ * 8), rows of an append, beams of a request and continuations kept of one, tokens
+ * of the vocabulary. */
+#define I8MM_CACHE_MAX_PAGES 16777216
+#define I8MM_CACHE_MAX_PAGE 4096
+#define I8MM_CACHE_MAX_ROW 1048576
+#define I8MM_CACHE_MAX_SEQS 1048576
+#define I8MM_CACHE_MAX_HEAD 256
+#define I8MM_CACHE_MAX_APPEND 16777216
+#define I8MM_BEAM_MAX 64
+#define I8MM_BEAM_MAX_VOCAB 16777216
+
+/*
+ * Appends rows to their sequences' pages: for each i < s, with q = seq[i]
+ * (or i if seq is NULL) and t = pos[i], head a's features K[i][a d .. (a + 1) d)
+ * go to slot t % page of page tables[q][t / page], and V's likewise.
+ *
+ * K, V: [s, kv_heads d] of `type` (I8MM_F16 or I8MM_BF16), row strides ldk,
+ * ldv, multiples of 8; all 16-byte aligned. seq, pos: [s] int32. A row whose
+ * q is outside [0, n), whose t is outside [0, max_pages page) or whose page
+ * number names no page is left out. Rows that go to the same slot: each 16
+ * bytes are one of theirs. Slots that no row goes to keep what they hold.
+ */
+i8mm_status i8mm_cache_append(const void* K, int64_t ldk, const void* V, int64_t ldv, int32_t type, int64_t s,
+                              int64_t kv_heads, int64_t d, const int32_t* seq, const int32_t* pos,
+                              const int32_t* tables, int64_t ldt, int64_t n, int64_t max_pages,
+                              void* K_pages, int64_t k_stride, void* V_pages, int64_t v_stride, int64_t n_pages,
+                              int64_t page, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_cache_fork (0 for bad arguments). */
+size_t i8mm_cache_fork_workspace_bytes(int64_t n, int64_t n_out, int64_t n_pages);
+
+/*
+ * The next step's sequences from this one's: sequences are kept, forked,
+ * reordered and freed, and grow by new tokens.
+ *
+ * New sequence j < n_out goes on from sequence parents[j] (from j if parents
+ * is NULL): it has that one's length and pages. A parent outside [0, n) gives
+ * an empty sequence; a sequence that nobody goes on from is freed. refs_out is
+ * refs, less one for each entry in use of the old tables and plus one for each
+ * of the new. Then, in the order of j, each sequence with grow[j] > 0 (grow
+ * NULL: none) gets room for that many tokens more:
+ *   - its last page, if that is not full, is written next. If others hold that
+ *     page too, it takes a copy: a fresh page with the same contents in every
+ *     pool. Of the sequences that grow in one page the last keeps it if the
+ *     others leave it no other holder.
+ *   - then fresh pages follow, up to ceil((len + grow) / page).
+ * Fresh pages are the free ones (by refs_out, before any are taken) from the
+ * lowest up. A sequence that would exceed max_pages pages does not grow, nor
+ * does one whose fresh pages, with those of the ones before it, are more than
+ * there are.
+ *
+ * tables_out: [n_out, max_pages] int32 (written; entries not in use are -1);
+ * lens_out: [n_out]; refs_out: [n_pages]; state: [4] int32: the pages still
+ * free, the fresh pages that were wanted beyond those free, the sequences that
+ * did not grow though asked to, the pages copied (all written). None of them
+ * may be an input. pools: host array of n_pools device pointers (up to 65536), 16-byte
+ * aligned; page_bytes, strides: host arrays of the bytes of a page in each
+ * (up to 2^32) and between its pages, multiples of 16. The arrays are read before the call
+ * returns. workspace: i8mm_cache_fork_workspace_bytes(...) bytes, 256-byte
+ * aligned, contents unspecified before and after.
+ */
+i8mm_status i8mm_cache_fork(const int32_t* tables, int64_t ldt, const int32_t* lens, const int32_t* refs, int64_t n,
+                            int64_t max_pages, int64_t n_pages, int64_t page, const int32_t* parents,
+                            const int32_t* grow, int64_t n_out, int32_t* tables_out, int64_t ldto, int32_t* lens_out,
+                            int32_t* refs_out, int32_t* state, void* const* pools, const int64_t* page_bytes,
+                            const int64_t* strides, int64_t n_pools, void* workspace, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_cache_compact (0 for bad arguments). */
+size_t i8mm_cache_compact_workspace_bytes(int64_t n_pages);
+
+/*
+ * Moves the pages in use to the front of the pools: with m of them (refs > 0),
+ * the k-th page in use from m on goes to the k-th free page below m, in every
+ * pool; the others stay.
+ *
+ * moved: [n_pages] int32 (written): each page's new number, -1 for a free one.
+ * tables_out: [n, max_pages] (written): tables with the new numbers (all
+ * entries; one that names no page stays as it is); may be tables itself, with
+ * the same stride. refs_out: [n_pages] (written): the counts in their new
+ * places; not refs. state: [2] int32 (written): m, and the pages moved.
+ * The pages moved from keep their contents. Pools as for i8mm_cache_fork.
+ * workspace: i8mm_cache_compact_workspace_bytes(n_pages) bytes, 256-byte
+ * aligned, contents unspecified before and after.
+ */
+i8mm_status i8mm_cache_compact(const int32_t* tables, int64_t ldt, int64_t n, int64_t max_pages, const int32_t* refs,
+                               int64_t n_pages, int32_t* tables_out, int64_t ldto, int32_t* refs_out, int32_t* moved,
+                               int32_t* state, void* const* pools, const int64_t* page_bytes, const int64_t* strides,
+                               int64_t n_pools, void* workspace, hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_decode_attention (0 for bad arguments). */
+size_t i8mm_decode_attention_workspace_bytes(int64_t n, int64_t heads, int64_t kv_heads, int64_t d);
+
+/*
+ * Attention of one new token of each sequence over its cached tokens: for head
+ * a of sequence i, with q = Q[i][a d .. (a + 1) d), the keys and values k_t, v_t
+ * of head a / (heads / kv_heads) and t < lens[i],
+ *   s_t = scale q . k_t + slopes[a] (t - (lens[i] - 1)),
+ *   out[i][a d ..] = sum_t exp(s_t - lse) v_t,  lse[i][a] = log sum_t exp(s_t).
+ * A sequence without tokens (or with none that a page is named for) gives
+ * out = 0 and lse = -inf.
+ *
+ * Q, out: [n, heads d] of `type` (I8MM_F16 or I8MM_BF16), row strides ldq, ldo,
+ * multiples of 8; 16-byte aligned. heads is a multiple of kv_heads. slopes:
+ * [heads] fp32, linear position biases, or NULL for none. scale: finite. lse:
+ * [n, heads] fp32 (written), or NULL. beams: sequences come in groups of this
+ * many neighbours, which divides n; pages that a group's tables share are read
+ * once for the group. It changes the speed alone; 1 is always right. workspace:
+ * i8mm_decode_attention_workspace_bytes(...) bytes, 256-byte aligned, contents
+ * unspecified before and after.
+ * What lies behind a sequence's last token never reaches it, NaN and infinity
+ * included.
+ */
+i8mm_status i8mm_decode_attention(const void* Q, int64_t ldq, int32_t type, int64_t n, int64_t heads, int64_t kv_heads,
+                                  int64_t d, const void* K_pages, int64_t k_stride, const void* V_pages,
+                                  int64_t v_stride, int64_t n_pages, int64_t page, const int32_t* tables, int64_t ldt,
+                                  int64_t max_pages, const int32_t* lens, int64_t beams, float scale,
+                                  const float* slopes, void* out, int64_t ldo, float* lse, void* workspace,
+                                  hipStream_t stream);
+
+/* Bytes of device workspace of i8mm_beam_select (0 for bad arguments). */
+size_t i8mm_beam_select_workspace_bytes(int64_t n, int64_t beams, int64_t vocab, int64_t k);
+
+/*
+ * Beam search's selection: for request b < n, of the continuations of its beams
+ * i < beams by the tokens v < vocab the k with the largest
+ *   t = scores[b][i] + x_v - log sum_u exp(x_u),  x = logits[b beams + i],
+ * from the largest down, ties from the lowest (i, v) up.
+ *
+ * logits: [n beams, vocab] of `type` (any i8mm_dtype), row stride ld. scores:
+ * [n, beams] fp32. k: up to I8MM_BEAM_MAX and beams * vocab. scores_out: [n, k]
+ * fp32 (written, not scores): t; parents: [n, k] int32 (written): b beams + i, as
+ * i8mm_cache_fork takes them; tokens: [n, k] int32 (written): v. A logit of -inf
+ * gives t = -inf. A beam whose score is not finite, or whose logits hold a NaN
+ * or +inf or are all -inf, gives t = -inf for each of its tokens.
+ * history: [n beams, T] int32, row stride ldh, the beams' tokens so far, and
+ * history_out: [n k, T + 1] (written, not history): the parents' rows and the
+ * new tokens; NULL history_out for none (history, ldh, T and ldho are then not
+ * looked at). Sums are fp32 over parts of a row and fp64 over the parts; t is
+ * compared in fp64. workspace: i8mm_beam_select_workspace_bytes(...) bytes,
+ * 256-byte aligned, contents unspecified before and after.
+ */
+i8mm_status i8mm_beam_select(const void* logits, int64_t ld, int32_t type, int64_t n, int64_t beams, int64_t vocab,
+                             const float* scores, int64_t k, float* scores_out, int32_t* parents, int32_t* tokens,
+                             const int32_t* history, int64_t ldh, int64_t T, int32_t* history_out, int64_t ldho,
+                             void* workspace, hipStream_t stream);
+
 /* Library version string (static storage). */
 const char* i8mm_version(void);
 

@@ -53,6 +53,12 @@ __all__ = [
     "lora_backward",
     "LORA_MAX_RANK",
     "clip_grad_norm",
+    "cache_append",
+    "cache_fork",
+    "cache_compact",
+    "decode_attention",
+    "beam_select",
+    "BEAM_MAX",
     "forward_workspace",
     "forward_workspace_views",
     "x_o_stride",
@@ -82,6 +88,9 @@ NOALLOC_SCRATCH_BYTES = _native.header_define("I8MM_NOALLOC_SCRATCH_BYTES")
 INLINE_QUANT_MIN_ROWS = _native.header_define("I8MM_INLINE_QUANT_MIN_ROWS")
 # Largest rank of the adapters (I8MM_LORA_MAX_RANK).
 LORA_MAX_RANK = _native.header_define("I8MM_LORA_MAX_RANK")
+
+# Most beams of a request, and continuations kept of one (I8MM_BEAM_MAX).
+BEAM_MAX = _native.header_define("I8MM_BEAM_MAX")
 
 
 class I8MMError(RuntimeError):
@@ -873,3 +882,231 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
                                   _raw_stream(dev))
     _check(st, "clip_grad_norm")
     return total
+
+
+# ---------------------------------------------------------------- decoding between int8 layers
+#
+# A paged cache: K_pages and V_pages [n_pages, kv_heads, page, d] (a page's own
+# part dense, any stride between pages), tables int32 [n, max_pages], lens int32
+# [n], refs int32 [n_pages].
+
+def _pages(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> Tuple[int, int]:
+    """(pointer, elements between pages) of a pool of pages."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device or t.dtype != dtype or t.dim() != 4 or (shape is not None and t.shape != shape):
+        want = "[n_pages, kv_heads, page, d]" if shape is None else str(tuple(shape))
+        raise ValueError(f"{name} must be {dtype} of shape {want} on cuda:{device} "
+                         f"(got {t.dtype} of shape {tuple(t.shape)} on {t.device})")
+    if not t.is_contiguous() and not (t.shape[0] and t[0].is_contiguous()):
+        raise ValueError(f"{name} must hold each page without gaps (strides {t.stride()})")
+    dense = t.shape[1] * t.shape[2] * t.shape[3]
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else dense
+
+
+def _pool_table(pools: Sequence[torch.Tensor], n_pages: int, device: int):
+    """(pointers, bytes of a page, bytes between pages) of tensors [n_pages, ...], as host arrays."""
+    at, size, step = array.array("Q"), array.array("q"), array.array("q")
+    for t in pools:
+        if t.get_device() != device or t.dim() < 1 or t.shape[0] != n_pages or not t[0].is_contiguous():
+            raise ValueError(f"pools must be tensors of {n_pages} pages without gaps in them on the current GPU, cuda:{device}")
+        e = t.element_size()
+        at.append(t.data_ptr())
+        size.append(t.numel() // n_pages * e)
+        step.append(t.stride(0) * e if n_pages > 1 else size[-1])
+    return at, size, step
+
+
+def _ints(t: Optional[torch.Tensor], name: str, n: int, device: int) -> Optional[int]:
+    return None if t is None else _dense(t, name, torch.int32, (n,), device)
+
+
+def _new_or(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype: torch.dtype, device: int) -> torch.Tensor:
+    """The caller's dense output, checked, or a new one."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _dense(t, name, dtype, shape, device)
+    return t
+
+
+def cache_append(K: torch.Tensor, V: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor, tables: torch.Tensor,
+                 pos: torch.Tensor, seq: Optional[torch.Tensor] = None) -> None:
+    """Row i of K and V [s, kv_heads d] (fp16 or bf16; rows may be strided, as
+    parts of a fused projection's rows are) goes to position pos[i] of sequence
+    seq[i] (None: i): into slot pos[i] % page of the page that `tables` names.
+    Rows whose sequence, position or page does not exist are left out. pos and
+    seq are int32 [s]."""
+    dev = _gpu_of(K, "K", _LORA_TYPES)
+    k, sk = _pages(K_pages, "K_pages", K.dtype, None, dev)
+    v, sv = _pages(V_pages, "V_pages", K.dtype, K_pages.shape, dev)
+    P, kv, page, d = K_pages.shape
+    s = K.shape[0]
+    x, ldk = _matrix(K, "K", K.dtype, (s, kv * d), dev)
+    y, ldv = _matrix(V, "V", K.dtype, (s, kv * d), dev)
+    n, M = tables.shape
+    t, ldt = _matrix(tables, "tables", torch.int32, (n, M), dev)
+    st = _lib.i8mm_cache_append(x, ldk, y, ldv, _DTYPES[K.dtype], s, kv, d, _ints(seq, "seq", s, dev), _ints(pos, "pos", s, dev),
+                                t, ldt, n, M, k, sk, v, sv, P, page, _raw_stream(dev))
+    _check(st, "cache_append")
+
+
+def cache_fork_workspace(n: int, n_out: int, n_pages: int) -> int:
+    """Bytes of workspace that cache_fork needs."""
+    return _lib.i8mm_cache_fork_workspace_bytes(n, n_out, n_pages)
+
+
+def cache_fork(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page: int, parents: Optional[torch.Tensor] = None,
+               grow: Optional[torch.Tensor] = None, pools: Sequence[torch.Tensor] = (),
+               tables_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+               refs_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The next step's sequences: number j goes on from sequence parents[j]
+    (int32; None: j; outside [0, n): empty) and grows by grow[j] tokens (int32;
+    None: 0). Pages are shared, freed and allocated by count, and a last page
+    that is written next while others hold it is copied in every tensor of
+    `pools` ([n_pages, ...], any type, each page a multiple of 16 bytes).
+    Returns (tables, lens, refs, state): state int32 [4] holds the pages still
+    free, the pages short, the sequences that could not grow (they keep their
+    length) and the pages copied. The outputs may not be the inputs. A
+    workspace, if given, is a uint8 tensor of cache_fork_workspace(n, n_out,
+    n_pages) bytes or more."""
+    dev = _gpu_of(tables, "tables", (torch.int32,))
+    n, M = tables.shape
+    P = refs.numel()
+    t, ldt = _matrix(tables, "tables", torch.int32, (n, M), dev)
+    r, l = _ints(refs, "refs", P, dev), _ints(lens, "lens", n, dev)
+    m = n if parents is None and grow is None else (grow if parents is None else parents).numel()
+    p, g = _ints(parents, "parents", m, dev), _ints(grow, "grow", m, dev)
+    at, size, step = _pool_table(pools, P, dev)
+    if tables_out is None:
+        tables_out = tables.new_empty((m, M))
+    to, ldto = _matrix(tables_out, "tables_out", torch.int32, (m, M), dev)
+    lens_out = _new_or(lens_out, "lens_out", lens, (m,), torch.int32, dev)
+    refs_out = _new_or(refs_out, "refs_out", refs, (P,), torch.int32, dev)
+    state = refs.new_empty(4)
+    workspace = _scratch(cache_fork_workspace(n, m, P), "cache_fork", workspace, tables.device)
+    st = _lib.i8mm_cache_fork(t, ldt, l, r, n, M, P, page, p, g, m, to, ldto, lens_out.data_ptr(), refs_out.data_ptr(),
+                              state.data_ptr(), at.buffer_info()[0], size.buffer_info()[0], step.buffer_info()[0], len(at),
+                              workspace.data_ptr(), _raw_stream(dev))
+    _check(st, "cache_fork")
+    return tables_out, lens_out, refs_out, state
+
+
+def cache_compact_workspace(n_pages: int) -> int:
+    """Bytes of workspace that cache_compact needs."""
+    return _lib.i8mm_cache_compact_workspace_bytes(n_pages)
+
+
+def cache_compact(tables: torch.Tensor, refs: torch.Tensor, pools: Sequence[torch.Tensor] = (),
+                  tables_out: Optional[torch.Tensor] = None, refs_out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Moves the pages in use (refs > 0) to the front of the pools. Returns
+    (tables, refs, moved, state) with the new page numbers: moved int32
+    [n_pages] gives each page's (-1: free), state int32 [2] the pages in use and
+    the pages moved. tables_out may be tables; refs_out may not be refs. A
+    workspace, if given, is a uint8 tensor of cache_compact_workspace(n_pages)
+    bytes or more."""
+    dev = _gpu_of(tables, "tables", (torch.int32,))
+    n, M = tables.shape
+    P = refs.numel()
+    t, ldt = _matrix(tables, "tables", torch.int32, (n, M), dev)
+    r = _ints(refs, "refs", P, dev)
+    at, size, step = _pool_table(pools, P, dev)
+    if tables_out is None:
+        tables_out = tables.new_empty((n, M))
+    to, ldto = _matrix(tables_out, "tables_out", torch.int32, (n, M), dev)
+    refs_out = _new_or(refs_out, "refs_out", refs, (P,), torch.int32, dev)
+    moved, state = refs.new_empty(P), refs.new_empty(2)
+    workspace = _scratch(cache_compact_workspace(P), "cache_compact", workspace, tables.device)
+    st = _lib.i8mm_cache_compact(t, ldt, n, M, r, P, to, ldto, refs_out.data_ptr(), moved.data_ptr(), state.data_ptr(),
+                                 at.buffer_info()[0], size.buffer_info()[0], step.buffer_info()[0], len(at),
+                                 workspace.data_ptr(), _raw_stream(dev))
+    _check(st, "cache_compact")
+    return tables_out, refs_out, moved, state
+
+
+def decode_attention_workspace(n: int, heads: int, kv_heads: int, d: int) -> int:
+    """Bytes of workspace that decode_attention needs."""
+    return _lib.i8mm_decode_attention_workspace_bytes(n, heads, kv_heads, d)
+
+
+def decode_attention(q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
+                     scale: Optional[float] = None, slopes: Optional[torch.Tensor] = None, beams: int = 1,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of one new token of each of n sequences, q [n, heads d] (fp16
+    or bf16; rows may be strided), over its lens[i] cached tokens, the new one
+    among them; heads share keys and values in groups of heads / kv_heads.
+    scale None: 1 / sqrt(d). slopes: fp32 [heads], linear position biases
+    slope (t - (len - 1)), or None. Returns (out [n, heads d] of q's type, lse
+    fp32 [n, heads]); a sequence without tokens gives 0 and -inf. beams says
+    that sequences come in groups of so many neighbours which may share pages
+    (read once for the group); it changes the speed alone. A workspace, if
+    given, is a uint8 tensor of decode_attention_workspace(n, heads, kv_heads,
+    d) bytes or more."""
+    dev = _gpu_of(q, "q", _LORA_TYPES)
+    k, sk = _pages(K_pages, "K_pages", q.dtype, None, dev)
+    v, sv = _pages(V_pages, "V_pages", q.dtype, K_pages.shape, dev)
+    P, kv, page, d = K_pages.shape
+    n, w = q.shape
+    heads = w // d if d else 0
+    x, ldq = _matrix(q, "q", q.dtype, (n, heads * d), dev)
+    M = tables.shape[1]
+    t, ldt = _matrix(tables, "tables", torch.int32, (n, M), dev)
+    if out is None:
+        out = q.new_empty((n, w))
+        y, ldo = out.data_ptr(), w
+    else:
+        y, ldo = _matrix(out, "out", q.dtype, (n, w), dev)
+    lse = _new_or(lse, "lse", q, (n, heads), torch.float32, dev)
+    sl = None if slopes is None else _dense(slopes, "slopes", torch.float32, (heads,), dev)
+    workspace = _scratch(decode_attention_workspace(n, heads, kv, d), "decode_attention", workspace, q.device)
+    st = _lib.i8mm_decode_attention(x, ldq, _DTYPES[q.dtype], n, heads, kv, d, k, sk, v, sv, P, page, t, ldt, M,
+                                    _ints(lens, "lens", n, dev), beams, d ** -0.5 if scale is None else scale, sl, y, ldo,
+                                    lse.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
+    _check(st, "decode_attention")
+    return out, lse
+
+
+def beam_select_workspace(n: int, beams: int, vocab: int, k: int) -> int:
+    """Bytes of workspace that beam_select needs."""
+    return _lib.i8mm_beam_select_workspace_bytes(n, beams, vocab, k)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = None, history: Optional[torch.Tensor] = None,
+                scores_out: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                tokens: Optional[torch.Tensor] = None, history_out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Of each request's continuations, scores [n, beams] (fp32) plus the log
+    softmax of logits [n beams, vocab] (fp16, bf16 or fp32; rows may be
+    strided), the k best (None: as many as there are beams), from the largest
+    down, ties from the lowest (beam, token) up. Returns (scores fp32 [n, k],
+    parents int32 [n, k], tokens int32 [n, k], history): parents are row
+    numbers of `logits`, as cache_fork takes them; history int32 [n beams, T],
+    if given, comes back as [n k, T + 1], each row its parent's and the new
+    token. A workspace, if given, is a uint8 tensor of beam_select_workspace(n,
+    beams, vocab, k) bytes or more."""
+    dev = _gpu_of(logits, "logits", _DTYPES)
+    n, beams = scores.shape
+    vocab = logits.shape[1]
+    k = beams if k is None else k
+    x, ld = _matrix(logits, "logits", logits.dtype, (n * beams, vocab), dev)
+    sc = _dense(scores, "scores", torch.float32, (n, beams), dev)
+    scores_out = _new_or(scores_out, "scores_out", scores, (n, k), torch.float32, dev)
+    parents = _new_or(parents, "parents", scores, (n, k), torch.int32, dev)
+    tokens = _new_or(tokens, "tokens", scores, (n, k), torch.int32, dev)
+    h = ho = None
+    T = ldh = ldho = 0
+    if history is not None:
+        T = history.shape[1]
+        h, ldh = _matrix(history, "history", torch.int32, (n * beams, T), dev)
+        if history_out is None:
+            history_out = history.new_empty((n * k, T + 1))
+        ho, ldho = _matrix(history_out, "history_out", torch.int32, (n * k, T + 1), dev)
+    workspace = _scratch(beam_select_workspace(n, beams, vocab, k), "beam_select", workspace, logits.device)
+    st = _lib.i8mm_beam_select(x, ld, _DTYPES[logits.dtype], n, beams, vocab, sc, k, scores_out.data_ptr(), parents.data_ptr(),
+                               tokens.data_ptr(), h, ldh, T, ho, ldho, workspace.data_ptr(), _raw_stream(dev))
+    _check(st, "beam_select")
+    return scores_out, parents, tokens, history_out if history is not None else None

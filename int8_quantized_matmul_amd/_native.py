@@ -58,6 +58,20 @@ _SIGNATURES = {
                                    c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p]),
     "i8mm_clip_grad_norm_workspace_bytes": (c_size, [c_p, c_i64]),
     "i8mm_clip_grad_norm": (c_int, [c_p, c_p, c_p, c_p, c_i64, c_f, c_p, c_p, c_p]),
+    "i8mm_cache_append": (c_int, [c_p, c_i64, c_p, c_i64, c_i32, c_i64, c_i64, c_i64, c_p, c_p, c_p, c_i64, c_i64, c_i64,
+                                  c_p, c_i64, c_p, c_i64, c_i64, c_i64, c_p]),
+    "i8mm_cache_fork_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "i8mm_cache_fork": (c_int, [c_p, c_i64, c_p, c_p, c_i64, c_i64, c_i64, c_i64, c_p, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p,
+                                c_p, c_p, c_p, c_i64, c_p, c_p]),
+    "i8mm_cache_compact_workspace_bytes": (c_size, [c_i64]),
+    "i8mm_cache_compact": (c_int, [c_p, c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_i64,
+                                   c_p, c_p]),
+    "i8mm_decode_attention_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64]),
+    "i8mm_decode_attention": (c_int, [c_p, c_i64, c_i32, c_i64, c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_i64, c_i64,
+                                      c_p, c_i64, c_i64, c_p, c_i64, c_f, c_p, c_p, c_i64, c_p, c_p, c_p]),
+    "i8mm_beam_select_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64]),
+    "i8mm_beam_select": (c_int, [c_p, c_i64, c_i32, c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p, c_i64, c_i64, c_p,
+                                 c_i64, c_p, c_p]),
     "i8mm_test_fail_product_launches": (None, [c_int]),
     "i8mm_version": (ctypes.c_char_p, []),
     "i8mm_status_string": (ctypes.c_char_p, [c_int]),

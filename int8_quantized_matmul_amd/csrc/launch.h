@@ -193,4 +193,111 @@ int64_t clip_parts(int64_t n);
 hipError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* numel, const int32_t* types,
                                  int64_t n, float max_norm, void* workspace, float* total, hipStream_t stream);
 
+// Decoding between int8 layers. A paged cache holds keys and values as
+// [n_pages][kv_heads][page][d], with a stride between pages; a sequence's row of
+// `tables` names its pages in order.
+
+// Rows of K and V [s, kv_heads d] into the pages of the sequences seq[i] (or i)
+// at the positions pos[i].
+struct AppendArgs {
+    const void *K, *V;
+    int64_t ldk, ldv;
+    int element_bytes;
+    int64_t s;
+    int kv_heads, d;
+    const int32_t *seq, *pos;       // seq may be null
+    const int32_t* tables;
+    int64_t ldt;
+    int64_t n;
+    int max_pages;
+    void *K_pages, *V_pages;
+    int64_t k_stride, v_stride;
+    int n_pages, page;
+};
+hipError_t launch_cache_append(const AppendArgs& a, hipStream_t stream);
+
+// Page pools: n device pointers, a page's bytes and the bytes between pages
+// (host arrays, read before the call returns).
+struct Pools {
+    void* const* at;
+    const int64_t* bytes;
+    const int64_t* strides;
+    int64_t n;
+};
+
+struct ForkArgs {
+    const int32_t* tables;
+    int64_t ldt;
+    const int32_t *lens, *refs;
+    int64_t n;
+    int max_pages, n_pages, page;
+    const int32_t *parents, *grow;  // each may be null
+    int64_t n_out;
+    int32_t* tables_out;
+    int64_t ldto;
+    int32_t *lens_out, *refs_out, *state;
+};
+size_t cache_fork_scratch(int64_t n, int64_t n_out, int64_t n_pages);
+hipError_t launch_cache_fork(const ForkArgs& a, const Pools& pools, void* workspace, hipStream_t stream);
+
+struct CompactArgs {
+    const int32_t* tables;
+    int64_t ldt;
+    int64_t n;
+    int max_pages;
+    const int32_t* refs;
+    int n_pages;
+    int32_t* tables_out;
+    int64_t ldto;
+    int32_t *refs_out, *moved, *state;
+};
+size_t cache_compact_scratch(int64_t n_pages);
+hipError_t launch_cache_compact(const CompactArgs& a, const Pools& pools, void* workspace, hipStream_t stream);
+
+// Attention of one query a sequence over its pages; slopes and lse may be null.
+struct AttendArgs {
+    const void* Q;
+    int64_t ldq;
+    Dtype type;
+    int64_t n;
+    int heads, kv_heads, d;
+    const void *K, *V;
+    int64_t k_stride, v_stride;
+    int n_pages, page;
+    const int32_t* tables;
+    int64_t ldt;
+    int max_pages;
+    const int32_t* lens;
+    int beams;
+    float scale;
+    const float* slopes;
+    void* out;
+    int64_t ldo;
+    float* lse;
+};
+size_t decode_attention_scratch(int64_t n, int heads, int kv_heads, int d);
+hipError_t launch_decode_attention(const AttendArgs& a, void* workspace, hipStream_t stream);
+
+// The k best of scores[b, i] + log_softmax(logits[b beams + i]) for each b;
+// history and history_out may be null.
+struct SelectArgs {
+    const void* logits;
+    int64_t ld;
+    Dtype type;
+    int64_t n;
+    int beams;
+    int vocab;
+    const float* scores;
+    int k;
+    float* scores_out;
+    int32_t *parents, *tokens;
+    const int32_t* history;
+    int64_t ldh;
+    int64_t T;
+    int32_t* history_out;
+    int64_t ldho;
+};
+size_t beam_select_scratch(int64_t n, int beams, int vocab, int k);
+hipError_t launch_beam_select(const SelectArgs& a, void* workspace, hipStream_t stream);
+
 }  // namespace i8mm
