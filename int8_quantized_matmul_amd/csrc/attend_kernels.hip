@@ -23,6 +23,8 @@
 
 #include "adapt_common.h"
 
+#include <type_traits>
+
 namespace i8mm {
 namespace {
 
@@ -32,6 +34,7 @@ constexpr int kHalf = 16;                        // keys of one matrix instructi
 constexpr int kStep = 2 * kHalf;                 // keys of a wavefront's step
 constexpr int kTile = kWaves * kStep;            // keys of a block's step
 constexpr int kCols = 16;                        // queries of one matrix instruction
+constexpr int kRunTiles = 24;                    // tiles of a run, if there are enough for several runs a block
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The probabilities of the running maximum are 2^kShift, so that in fp16 those
@@ -70,16 +73,24 @@ __device__ __forceinline__ float column_sum(float v) {
 // features of a value that a lane holds.
 template <int NC, int EL>
 struct Step {
-    v4u k[2][NC];            // half, chunk: 8 features of key l % 16
+    v4u k[2][NC];               // half, chunk: 8 features of key l % 16
     unsigned v[2][4][EL / 2];   // half, key 4 (l / 16) + r: features EL (l % 16) ..
-    int id[2];               // the halves' pages, -1 where there is none
-    int key;                 // the first half's first key
+    int id[2];                  // the halves' pages, -1 where there is none
+    int key;                    // the first half's first key
 };
 
-template <typename T, int NC, int EL>
+template <int EL>
 struct Sums {
     v4f o[EL];               // feature EL (4 (l / 16) + r) + e of query l % 16
     float m, l;              // maximum (in powers of 2) of the query; sum of this lane's keys
+};
+
+// What a wavefront's columns ask for.
+template <int NC>
+struct Queries {
+    v4u q[NC];               // 8 features of query l % 16
+    float scale, bias;       // times log2 e
+    int last;                // the query's own sequence's last key, which the biases count from
 };
 
 template <typename T, int NC, int EL, bool Full>
@@ -102,13 +113,14 @@ __device__ __forceinline__ void load_step(Step<NC, EL>& s, const AttendArgs& a, 
         for (int r = 0; r < 4; ++r) {
             const T* row = V + (4 * g + r) * a.d + EL * x;
             if constexpr (EL == 4) {
-                const v2u w = Full || 4 * x < a.d ? *reinterpret_cast<const v2u*>(row) : v2u{0, 0};
+                const v2u w = Full || 4 * x < a.d ? __builtin_nontemporal_load(reinterpret_cast<const v2u*>(row)) : v2u{0, 0};
                 s.v[h][r][0] = w[0];
                 s.v[h][r][1] = w[1];
             } else {
 #pragma unroll
                 for (int p = 0; p < EL / 8; ++p) {
-                    const v4u w = Full || EL * x + 8 * p < a.d ? *reinterpret_cast<const v4u*>(row + 8 * p) : v4u{0, 0, 0, 0};
+                    const v4u w = Full || EL * x + 8 * p < a.d ? __builtin_nontemporal_load(reinterpret_cast<const v4u*>(row + 8 * p))
+                                                                : v4u{0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s.v[h][r][4 * p + i] = w[i];
                 }
@@ -117,11 +129,10 @@ __device__ __forceinline__ void load_step(Step<NC, EL>& s, const AttendArgs& a, 
     }
 }
 
-// The step's part of the sums. bias: slope of this lane's query times log2(e);
-// last: the sequence's last key.
-template <typename T, int NC, int EL>
-__device__ __forceinline__ void add_step(Sums<T, NC, EL>& sum, Step<NC, EL>& s, const v4u (&q)[NC], float scale, float bias,
-                                         int last, int lane) {
+// The step's part of the sums. last: the last key that may be seen. Alone: the
+// step is that of some columns (`mine`), the others stay as they are.
+template <typename T, int NC, int EL, bool Alone>
+__device__ __forceinline__ void add_step(Sums<EL>& sum, Step<NC, EL>& s, const Queries<NC>& q, int last, bool mine, int lane) {
     typedef typename Vec8<T>::type vec;
     const int g = lane >> 4;
     float p[2][4];
@@ -129,15 +140,18 @@ __device__ __forceinline__ void add_step(Sums<T, NC, EL>& sum, Step<NC, EL>& s, 
     for (int h = 0; h < 2; ++h) {
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc = mma(__builtin_bit_cast(vec, s.k[h][c]), __builtin_bit_cast(vec, q[c]), acc);
-        const int from = s.key + h * kHalf + 4 * g - last;    // <= 0 for the sequence's keys
+        for (int c = 0; c < NC; ++c) acc = mma(__builtin_bit_cast(vec, s.k[h][c]), __builtin_bit_cast(vec, q.q[c]), acc);
+        const int key = s.key + h * kHalf + 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[h][r] = __builtin_fmaf(bias, static_cast<float>(from + r), acc[r] * scale);
+        for (int r = 0; r < 4; ++r) {
+            p[h][r] = __builtin_fmaf(q.bias, static_cast<float>(key + r - q.last), acc[r] * q.scale);
+            if (Alone) p[h][r] = mine ? p[h][r] : -INFINITY;
+        }
         if (s.id[h] < 0 || s.key + h * kHalf + kHalf - 1 > last) {
             // keys that are not there: no weight, and whatever their slots hold stays out of the sums
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool there = s.id[h] >= 0 && from + r <= 0;
+                const bool there = s.id[h] >= 0 && key + r <= last;
                 p[h][r] = there ? p[h][r] : -INFINITY;
 #pragma unroll
                 for (int i = 0; i < EL / 2; ++i) s.v[h][r][i] = there ? s.v[h][r][i] : 0u;
@@ -149,10 +163,11 @@ __device__ __forceinline__ void add_step(Sums<T, NC, EL>& sum, Step<NC, EL>& s, 
     most = fmaxf(column_max(most), sum.m);
     if (__any(most > sum.m)) {
         const float f = sum.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sum.m - most);
+        const float by = most == -INFINITY ? 1.0f : f;
         sum.m = most;
-        sum.l *= f;
+        sum.l *= by;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) sum.o[e] *= f;
+        for (int e = 0; e < EL; ++e) sum.o[e] *= by;
     }
     const float off = sum.m == -INFINITY ? 0.0f : sum.m - kShift;
     vec w;
@@ -172,113 +187,466 @@ __device__ __forceinline__ void add_step(Sums<T, NC, EL>& sum, Step<NC, EL>& s, 
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r) t[2 * h + r] = __builtin_amdgcn_perm(s.v[h][2 * r + 1][e / 2], s.v[h][2 * r][e / 2], pick);
-        sum.o[e] = mma(__builtin_bit_cast(vec, t), w, sum.o[e]);
+        const v4f o = mma(__builtin_bit_cast(vec, t), w, sum.o[e]);
+        // a NaN among these values times a weight of 0 must not reach the other columns
+        if (Alone) sum.o[e] = mine ? o : sum.o[e];
+        else sum.o[e] = o;
     }
 }
 
-template <typename T, int NC, int EL, bool Full>
-__global__ __launch_bounds__(kThreads) void k_attend(const AttendArgs a) {
-    __shared__ float s_o[kWaves][kCols][16 * EL];
-    __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
+// ---------------------------------------------------------------- how the work is split
+//
+// Sequences are taken in groups: `beams` of them that may share pages, as many as
+// their queries fill the 16 columns (one sequence if beams is 1). A group's tiles of
+// 128 keys are first those that all its sequences share, read once for all, then each
+// sequence's own. All groups, heads and tiles are one row of units, cut into equal
+// runs: lengths may differ as they like, and a few long sequences fill the chip as
+// well as many short ones. A run that covers all units of a (group, head) writes its
+// result; the others leave partial sums (at most two a run: of the one it starts in,
+// and of the one it ends in), which a second launch joins.
+
+struct Split {
+    int64_t groups;
+    int gb, chunks;          // sequences of a group at most, groups of `beams` sequences
+    int group, parts;        // heads that share a key-value head, in parts of 16
+    const int32_t* shared;   // [groups]: tiles that a group's sequences share (null: groups of one)
+    int cols;                // columns in use, at most
+    int rounds;              // runs of a block, at most
+    float* o;                // [runs][2][cols][d]: the partial sums
+    float* ml;               // [runs][2][cols][2]: their maximum and sum
+    struct Join {
+        int64_t group;
+        int head;            // key-value head and part
+        int first;           // the run with the first partial sums, -1: nothing to join
+    }* joins;                // [runs]
+};
+
+__device__ __forceinline__ int clamped_len(const AttendArgs& a, int64_t seq) {
+    const int len = a.lens[seq], most = a.max_pages * a.page;
+    return len < 0 ? 0 : len < most ? len : most;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+struct Group {
+    int64_t first;           // its first sequence
+    int n;                   // and how many they are
+};
+__device__ __forceinline__ Group group_at(const AttendArgs& a, const Split& w, int64_t gi) {
+    const int64_t r = gi / w.chunks;
+    const int c = static_cast<int>(gi - r * w.chunks) * w.gb;
+    return {r * a.beams + c, a.beams - c < w.gb ? a.beams - c : w.gb};
+}
+
+// Units of a group for one head: at least one, which writes the result of empty sequences.
+template <bool Beams>
+__device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Split& w, int64_t gi) {
+    int64_t u = 0;
+    if (Beams) {
+        const Group g = group_at(a, w, gi);
+        const int s = w.shared[gi];
+        u = s;
+        for (int b = 0; b < g.n; ++b) {
+            const int t = tiles_of(clamped_len(a, g.first + b)) - s;
+            u += t > 0 ? t : 0;
+        }
+    } else {
+        u = tiles_of(clamped_len(a, gi));
+    }
+    return u > 0 ? u : 1;
+}
+
+// The tiles that all sequences of a group share: the same keys of the same pages. A wavefront a group.
+__global__ __launch_bounds__(kThreads) void k_attend_shared(const AttendArgs a, const Split w, int32_t* shared) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6); gi < w.groups;
+         gi += static_cast<int64_t>(gridDim.x) * kWaves) {
+        const Group g = group_at(a, w, gi);
+        int least = clamped_len(a, g.first), most = least;
+        for (int b = 1; b < g.n; ++b) {
+            const int len = clamped_len(a, g.first + b);
+            least = len < least ? len : least;
+            most = len > most ? len : most;
+        }
+        // where lengths differ, a tile is shared as far as it is full for all
+        int keys = least == most ? tiles_of(most) * kTile : least / kTile * kTile;
+        const int used = ((keys < most ? keys : most) + a.page - 1) / a.page;
+        for (int c0 = 0; c0 < used; c0 += kWave) {
+            const int c = c0 + lane;
+            bool differ = false;
+            if (c < used) {
+                const int id = a.tables[g.first * a.ldt + c];
+                for (int b = 1; b < g.n; ++b) differ |= a.tables[(g.first + b) * a.ldt + c] != id;
+            }
+            const uint64_t any = __ballot(differ);
+            if (any) {
+                keys = (c0 + __builtin_ctzll(any)) * a.page / kTile * kTile;
+                break;
+            }
+        }
+        if (lane == 0) shared[gi] = keys / kTile;
+    }
+}
+
+template <int NC, int EL>
+struct Attend {
+    static constexpr int kWide = 16 * EL;
+    float o[kWaves][kCols][kWide];
+    float m[kWaves][kCols], l[kWaves][kCols];
+    int64_t scan[kWaves];
+    int64_t at_group, at_units;
+};
+
+// Joins the wavefronts' sums; f(column, feature, o, m, l) for each, o and l relative to 2^(m - kShift).
+template <int NC, int EL, typename F>
+__device__ __forceinline__ void join_waves(Attend<NC, EL>& s, const Sums<EL>& sum, int cols, int d, int wave, int lane, F&& f) {
+    const int x = lane & 15, g = lane >> 4;
+    const float l = column_sum(sum.l);
+    if (x < cols) {
+        if (g == 0) {
+            s.m[wave][x] = sum.m;
+            s.l[wave][x] = l;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) s.o[wave][x][EL * (4 * g + r) + e] = sum.o[e][r];
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < cols * d; k += kThreads) {
+        const int c = k / d, i = k - c * d;
+        float m = s.m[0][c];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s.m[w][c]);
+        float all = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float by = s.m[w][c] == -INFINITY ? (s.l[w][c] == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(s.m[w][c] - m);
+            all = __builtin_fmaf(by, s.l[w][c], all);
+            o = __builtin_fmaf(by, s.o[w][c][i], o);
+        }
+        f(c, i, o, m, all);
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_log2f(l) - kShift) * kLn2; }
+
+// Column c of a group's head: its sequence and head.
+struct Column {
+    int64_t seq;
+    int head;
+};
+__device__ __forceinline__ Column column_of(const Split& w, const Group& g, int kv, int part, int c) {
+    if (w.parts > 1) return {g.first, kv * w.group + part * kCols + c};
+    const int b = c / w.group;
+    return {g.first + b, kv * w.group + c - b * w.group};
+}
+
+template <typename T>
+__device__ __forceinline__ void put(const AttendArgs& a, const Column& c, int i, float o, float m, float l) {
+    static_cast<T*>(a.out)[c.seq * a.ldo + static_cast<int64_t>(c.head) * a.d + i] = static_cast<T>(l == 0.0f ? 0.0f : o / l);
+    if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum(m, l);
+}
+
+// Whole: each block takes whole (group, head)s, and nothing is left to join.
+template <typename T, int NC, int EL, bool Full, bool Beams, bool Whole>
+__global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const AttendArgs a, const Split w) {
+    __shared__ Attend<NC, EL> s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, g = lane >> 4;
-    const int group = a.heads / a.kv_heads, parts = (group + kCols - 1) / kCols;
-    const int64_t items = static_cast<int64_t>(a.n) * a.kv_heads * parts;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int part = static_cast<int>(item % parts);
-        const int kv = static_cast<int>(item / parts % a.kv_heads);
-        const int64_t i = item / parts / a.kv_heads;
-        const int cols = group - part * kCols < kCols ? group - part * kCols : kCols;
-        const int first = kv * group + part * kCols;            // the first column's head
-        const int most = a.max_pages * a.page;
-        const int len = a.lens[i] < most ? a.lens[i] : most;
+    const int heads = a.kv_heads * w.parts;
+    int64_t runs = gridDim.x, total = 0, before = 0, mine = 0, g0 = 0;
+    if (!Whole) {
+        // units of all groups: each thread sums some neighbours
+        const int64_t per = (w.groups + kThreads - 1) / kThreads;
+        g0 = threadIdx.x * per;
+        const int64_t g1 = g0 + per < w.groups ? g0 + per : w.groups;
+        for (int64_t k = g0; k < g1; ++k) mine += units_of<Beams>(a, w, k);
+        int64_t upto = mine;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const int64_t t = __shfl_up(upto, off, kWave);
+            if (lane >= off) upto += t;
+        }
+        if (lane == 63) s.scan[wave] = upto;
+        __syncthreads();
+        for (int k = 0; k < kWaves; ++k) {
+            if (k < wave) before += s.scan[k];
+            total += s.scan[k];
+        }
+        before += upto - mine;
+        total *= heads;
+        const int64_t rounds = total / (static_cast<int64_t>(gridDim.x) * kRunTiles);
+        runs *= rounds < 1 ? 1 : rounds < w.rounds ? rounds : w.rounds;
+        runs = total < runs ? total : runs;
+        for (int r = threadIdx.x; r < w.rounds; r += kThreads) w.joins[static_cast<int64_t>(r) * gridDim.x + blockIdx.x].first = -1;
+        __syncthreads();
+    }
+    for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
+    int64_t gi, u, end;                             // group; unit of the whole row, and where the run ends
+    int64_t units, head, v;                         // the group's units for a head, the head, unit within it
+    if (Whole) {
+        gi = run / heads;
+        head = run - gi * heads;
+        units = units_of<Beams>(a, w, gi);
+        v = 0;
+        u = 0;
+        end = units;
+    } else {
+        u = total * run / runs;
+        end = total * (run + 1) / runs;
+        const int64_t at = u / heads;
+        if (at >= before && at < before + mine) {
+            int64_t k = g0, from = before, n;
+            while (at >= from + (n = units_of<Beams>(a, w, k))) from += n, ++k;
+            s.at_group = k;
+            s.at_units = from;
+        }
+        __syncthreads();
+        gi = s.at_group;
+        units = units_of<Beams>(a, w, gi);
+        const int64_t rest = u - s.at_units * heads;
+        head = rest / units;
+        v = rest - head * units;
+    }
+    while (u < end) {
+        const Group grp = Beams ? group_at(a, w, gi) : Group{gi, 1};
+        const int kv = static_cast<int>(head / w.parts), part = static_cast<int>(head - static_cast<int64_t>(kv) * w.parts);
+        const int cols = w.parts > 1 ? (w.group - part * kCols < kCols ? w.group - part * kCols : kCols) : grp.n * w.group;
         const int64_t head_at = static_cast<int64_t>(kv) * a.page * a.d;
+        const Column col = column_of(w, grp, kv, part, x);
 
-        v4u q[NC];
-        const T* row = static_cast<const T*>(a.Q) + i * a.ldq + static_cast<int64_t>(first + x) * a.d;
+        Queries<NC> q;
+        const T* row = static_cast<const T*>(a.Q) + col.seq * a.ldq + static_cast<int64_t>(col.head) * a.d;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int f = 32 * c + 8 * g;
-            q[c] = x < cols && f < a.d ? *reinterpret_cast<const v4u*>(row + f) : v4u{0, 0, 0, 0};
+            q.q[c] = x < cols && f < a.d ? *reinterpret_cast<const v4u*>(row + f) : v4u{0, 0, 0, 0};
         }
-        const float bias = a.slopes && x < cols ? a.slopes[first + x] * kLog2e : 0.0f;
+        q.scale = a.scale * kLog2e;
+        q.bias = a.slopes && x < cols ? a.slopes[col.head] * kLog2e : 0.0f;
+        q.last = (Beams && x >= cols ? 0 : clamped_len(a, Beams ? col.seq : gi)) - 1;
 
-        Sums<T, NC, EL> sum;
+        Sums<EL> sum;
         sum.m = -INFINITY;
         sum.l = 0.0f;
 #pragma unroll
         for (int e = 0; e < EL; ++e) sum.o[e] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int key = wave * kStep; key < len; key += kTile) {
-            Step<NC, EL> s;
-            s.key = key;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int at = key + h * kHalf;
-                int id = at < len ? a.tables[i * a.ldt + at / a.page] : -1;
-                if (id >= a.n_pages) id = -1;
-                s.id[h] = __builtin_amdgcn_readfirstlane(id);
-            }
-            load_step<T, NC, EL, Full>(s, a, head_at, lane);
-            add_step<T, NC, EL>(sum, s, q, a.scale * kLog2e, bias, len - 1, lane);
-        }
-        sum.l = column_sum(sum.l);
 
-        if (x < cols) {
-            if (g == 0) {
-                s_m[wave][x] = sum.m;
-                s_l[wave][x] = sum.l;
+        // tiles t .. stop of sequence `seq`, for all columns or for those that are `mine`
+        const auto pass = [&](auto alone, int64_t seq, int t, int stop, int len, bool mine) {
+            constexpr bool kAlone = decltype(alone)::value;
+            int ids = -1, base = t - kWave;
+            const auto fetch = [&](Step<NC, EL>& st, int tile) {
+                if (tile - base >= kWave / 2) {          // the next 32 tiles' pages, two a lane pair
+                    base = tile;
+                    const int key = ((tile + (lane >> 1)) * kWaves + wave) * kStep + (lane & 1) * kHalf;
+                    ids = key < len && key >= 0 ? a.tables[seq * a.ldt + key / a.page] : -1;
+                    if (ids >= a.n_pages) ids = -1;
+                }
+                st.key = (tile * kWaves + wave) * kStep;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) st.id[h] = __builtin_amdgcn_readlane(ids, 2 * (tile - base) + h);
+                load_step<T, NC, EL, Full>(st, a, head_at, lane);
+            };
+            Step<NC, EL> p, n;
+            if (t < stop) fetch(p, t);
+            for (; t < stop; t += 2) {
+                if (t + 1 < stop) fetch(n, t + 1);
+                add_step<T, NC, EL, kAlone>(sum, p, q, len - 1, mine, lane);
+                if (t + 1 >= stop) break;
+                if (t + 2 < stop) fetch(p, t + 2);
+                add_step<T, NC, EL, kAlone>(sum, n, q, len - 1, mine, lane);
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int e = 0; e < EL; ++e) s_o[wave][x][EL * (4 * g + r) + e] = sum.o[e][r];
-        }
-        __syncthreads();
-        T* out = static_cast<T*>(a.out) + i * a.ldo + static_cast<int64_t>(first) * a.d;
-        for (int k = threadIdx.x; k < cols * a.d; k += kThreads) {
-            const int c = k / a.d, f = k % a.d;
-            float m = s_m[0][c];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][c]);
-            float l = 0.0f, o = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float by = s_m[w][c] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][c] - m);
-                l = __builtin_fmaf(by, s_l[w][c], l);
-                o = __builtin_fmaf(by, s_o[w][c][f], o);
+        };
+        const int64_t v1 = units - v < end - u ? units : v + (end - u);
+        if (!Beams) {
+            const int len = clamped_len(a, gi);
+            const int tiles = tiles_of(len);
+            pass(std::false_type{}, gi, static_cast<int>(v), static_cast<int>(v1 < tiles ? v1 : tiles), len, true);
+        } else {
+            const int shared = w.shared[gi];
+            if (v < shared)
+                pass(std::false_type{}, grp.first, static_cast<int>(v), static_cast<int>(v1 < shared ? v1 : shared),
+                     clamped_len(a, grp.first), true);
+            int64_t from = shared;
+            for (int b = 0; b < grp.n; ++b) {
+                const int len = clamped_len(a, grp.first + b);
+                const int own = tiles_of(len) > shared ? tiles_of(len) - shared : 0;
+                const int64_t lo = v > from ? v : from, hi = v1 < from + own ? v1 : from + own;
+                if (lo < hi)
+                    pass(std::true_type{}, grp.first + b, static_cast<int>(lo - from) + shared, static_cast<int>(hi - from) + shared,
+                         len, col.seq == grp.first + b && x < cols);
+                from += own;
             }
-            out[k] = static_cast<T>(l == 0.0f ? 0.0f : o / l);
-            if (f == 0 && a.lse) a.lse[i * a.heads + first + c] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l) - kShift) * kLn2;
         }
-        __syncthreads();
+
+        if (Whole || v1 - v == units) {
+            join_waves<NC, EL>(s, sum, cols, a.d, wave, lane, [&](int c, int i, float o, float m, float l) {
+                put<T>(a, column_of(w, grp, kv, part, c), i, o, m, l);
+            });
+        } else {
+            const int64_t slot = (run * 2 + (v == 0)) * w.cols;
+            join_waves<NC, EL>(s, sum, cols, a.d, wave, lane, [&](int c, int i, float o, float m, float l) {
+                w.o[(slot + c) * a.d + i] = o;
+                if (i == 0) {
+                    w.ml[(slot + c) * 2] = m;
+                    w.ml[(slot + c) * 2 + 1] = l;
+                }
+            });
+            if (v > 0 && v1 == units && threadIdx.x == 0) {
+                // the run with the first unit, u - v: the last one that starts at or before it
+                w.joins[run] = {gi, static_cast<int>(head), static_cast<int>(((u - v + 1) * runs - 1) / total)};
+            }
+        }
+        u += v1 - v;
+        v = 0;
+        if (++head == heads) {
+            head = 0;
+            ++gi;
+            if (u < end) units = units_of<Beams>(a, w, gi);
+        }
+    }
     }
 }
 
-template <typename T, int NC, int EL>
-hipError_t attend(const AttendArgs& a, hipStream_t stream) {
-    const int parts = (a.heads / a.kv_heads + kCols - 1) / kCols;
-    const int64_t items = static_cast<int64_t>(a.n) * a.kv_heads * parts;
-    const unsigned blocks = static_cast<unsigned>(items < 4096 ? items : 4096);
-    if (a.d == 32 * NC && a.d == 16 * EL) k_attend<T, NC, EL, true><<<blocks, kThreads, 0, stream>>>(a);
-    else k_attend<T, NC, EL, false><<<blocks, kThreads, 0, stream>>>(a);
+// The partial sums of one (group, head): the first run's second ones, and the others'
+// first ones. Every 16 bytes of the result are summed by one thread, or, where there are
+// fewer of them than threads, by several that take the runs in turn.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, const Split w) {
+    __shared__ float s_m[kCols], s_l[kCols];
+    __shared__ v4f s_o[kThreads];
+    const Split::Join j = w.joins[blockIdx.x];
+    if (j.first < 0) return;
+    const Group grp = group_at(a, w, j.group);
+    const int kv = j.head / w.parts, part = j.head - kv * w.parts;
+    const int cols = w.parts > 1 ? (w.group - part * kCols < kCols ? w.group - part * kCols : kCols) : grp.n * w.group;
+    const int n = static_cast<int>(blockIdx.x) - j.first + 1;
+    const auto slot = [&](int b) { return (static_cast<int64_t>(j.first + b) * 2 + (b == 0)) * w.cols; };
+    const int lane = threadIdx.x & 63;
+    for (int c = threadIdx.x >> 6; c < cols; c += kWaves) {
+        float m = -INFINITY, l = 0.0f;
+        for (int b = lane; b < n; b += kWave) m = fmaxf(m, w.ml[(slot(b) + c) * 2]);
+        m = wave_max(m);
+        for (int b = lane; b < n; b += kWave) {
+            const float* p = w.ml + (slot(b) + c) * 2;
+            l += p[0] == -INFINITY ? p[1] : p[1] * __builtin_amdgcn_exp2f(p[0] - m);
+        }
+        l = wave_sum(l);
+        if (lane == 0) {
+            s_m[c] = m;
+            s_l[c] = l;
+        }
+    }
+    __syncthreads();
+    const int quads = a.d / 4, all = cols * quads, sharers = all < kThreads ? kThreads / all : 1;
+    for (int k0 = 0; k0 < all; k0 += kThreads) {
+        const int by = static_cast<int>(threadIdx.x) / all, k = sharers > 1 ? static_cast<int>(threadIdx.x) - by * all : k0 + static_cast<int>(threadIdx.x);
+        const bool there = sharers > 1 ? by < sharers : k < all;
+        const int c = k / quads, i = 4 * (k - c * quads);
+        v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (there) {
+#pragma unroll 4
+            for (int b = sharers > 1 ? by : 0; b < n; b += sharers) {
+                const int64_t at = slot(b) + c;
+                const float m = w.ml[at * 2], f = m == -INFINITY ? (w.ml[at * 2 + 1] == 0.0f ? 0.0f : 1.0f)
+                                                                   : __builtin_amdgcn_exp2f(m - s_m[c]);
+                o += *reinterpret_cast<const v4f*>(w.o + at * a.d + i) * f;
+            }
+        }
+        if (sharers > 1) {
+            s_o[threadIdx.x] = o;
+            __syncthreads();
+            if (by == 0)
+                for (int b = 1; b < sharers; ++b) o += s_o[b * all + k];
+        }
+        if (there && (sharers == 1 || by == 0)) {
+            const Column col = column_of(w, grp, kv, part, c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put<T>(a, col, i + e, o[e], s_m[c], s_l[c]);
+        }
+    }
+}
+
+// Blocks of the split kernel: as many as are resident at once.
+template <int EL>
+constexpr int kBlocks = EL == 16 ? 256 : 512;
+
+// Rows of partial sums that the workspace holds: a run leaves two of each of its columns.
+constexpr int kSumRows = 32768;
+
+int most_rounds(int cols, int blocks) {
+    const int r = kSumRows / (2 * cols * blocks);
+    return r < 1 ? 1 : r < 8 ? r : 8;
+}
+
+// Up to this many keys a sequence a block takes whole (group, head)s.
+constexpr int kWholeKeys = 4 * kTile;
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+
+template <typename T, int NC, int EL, bool Full>
+hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_t stream) {
+    w.group = a.heads / a.kv_heads;
+    w.parts = (w.group + kCols - 1) / kCols;
+    const int heads = a.kv_heads * w.parts;
+    if (static_cast<int64_t>(a.max_pages) * a.page <= kWholeKeys && a.n * heads < (int64_t(1) << 23)) {
+        w.groups = a.n;
+        w.gb = w.chunks = 1;
+        AttendArgs one = a;
+        one.beams = 1;
+        k_attend<T, NC, EL, Full, false, true><<<static_cast<unsigned>(a.n * heads), kThreads, 0, stream>>>(one, w);
+        return hipGetLastError();
+    }
+    w.gb = w.parts > 1 ? 1 : kCols / w.group < a.beams ? kCols / w.group : a.beams;
+    w.chunks = (a.beams + w.gb - 1) / w.gb;
+    w.groups = a.n / a.beams * w.chunks;
+    w.cols = w.parts > 1 ? kCols : w.gb * w.group;
+    w.rounds = most_rounds(w.cols, kBlocks<EL>);
+    char* at = static_cast<char*>(workspace);
+    w.o = reinterpret_cast<float*>(at);
+    w.ml = reinterpret_cast<float*>(at += round256(static_cast<int64_t>(kSumRows) * a.d * 4));
+    w.joins = reinterpret_cast<Split::Join*>(at += round256(static_cast<int64_t>(kSumRows) * 2 * 4));
+    at += round256(kSumRows / 2 * sizeof(Split::Join));
+    if (w.gb > 1) {
+        int32_t* shared = reinterpret_cast<int32_t*>(at);
+        w.shared = shared;
+        const int64_t blocks = (w.groups + kWaves - 1) / kWaves;
+        k_attend_shared<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kThreads, 0, stream>>>(a, w, shared);
+        k_attend<T, NC, EL, Full, true, false><<<kBlocks<EL>, kThreads, 0, stream>>>(a, w);
+    } else {
+        k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL>, kThreads, 0, stream>>>(a, w);
+    }
+    k_attend_join<T><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
     return hipGetLastError();
 }
 
+template <typename T, int NC, int EL>
+hipError_t attend(const AttendArgs& a, void* workspace, hipStream_t stream) {
+    return a.d == 32 * NC && a.d == 16 * EL ? attend_with<T, NC, EL, true>(a, {}, workspace, stream)
+                                            : attend_with<T, NC, EL, false>(a, {}, workspace, stream);
+}
+
 template <typename T>
-hipError_t attend_type(const AttendArgs& a, hipStream_t stream) {
-    if (a.d <= 64) return attend<T, 2, 4>(a, stream);
-    if (a.d <= 96) return attend<T, 3, 8>(a, stream);
-    if (a.d <= 128) return attend<T, 4, 8>(a, stream);
-    return attend<T, 8, 16>(a, stream);
+hipError_t attend_type(const AttendArgs& a, void* workspace, hipStream_t stream) {
+    if (a.d <= 64) return attend<T, 2, 4>(a, workspace, stream);
+    if (a.d <= 96) return attend<T, 3, 8>(a, workspace, stream);
+    if (a.d <= 128) return attend<T, 4, 8>(a, workspace, stream);
+    return attend<T, 8, 16>(a, workspace, stream);
 }
 
 }  // namespace
 
-size_t decode_attention_scratch(int64_t, int, int, int) { return 256; }
+size_t decode_attention_scratch(int64_t n, int, int, int d) {
+    return static_cast<size_t>(round256(static_cast<int64_t>(kSumRows) * d * 4) + round256(static_cast<int64_t>(kSumRows) * 2 * 4) +
+                               round256(kSumRows / 2 * sizeof(Split::Join)) + round256(4 * n) + 256);
+}
 
-hipError_t launch_decode_attention(const AttendArgs& a, void*, hipStream_t stream) {
+hipError_t launch_decode_attention(const AttendArgs& a, void* workspace, hipStream_t stream) {
     if (a.n == 0) return hipSuccess;
-    return a.type == Dtype::F16 ? attend_type<_Float16>(a, stream) : attend_type<__bf16>(a, stream);
+    return a.type == Dtype::F16 ? attend_type<_Float16>(a, workspace, stream) : attend_type<__bf16>(a, workspace, stream);
 }
 
 }  // namespace i8mm
