@@ -233,6 +233,7 @@ struct Group {
     int n;                   // and how many they are
 };
 __device__ __forceinline__ Group group_at(const AttendArgs& a, const Split& w, int64_t gi) {
+    if (w.chunks == 1) return {gi * a.beams, a.beams};
     const int64_t r = gi / w.chunks;
     const int c = static_cast<int>(gi - r * w.chunks) * w.gb;
     return {r * a.beams + c, a.beams - c < w.gb ? a.beams - c : w.gb};
@@ -349,6 +350,10 @@ __device__ __forceinline__ void put(const AttendArgs& a, const Column& c, int i,
     if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum(m, l);
 }
 
+// Runs of the split kernel in multiples of the blocks that are resident at once.
+template <int EL>
+constexpr int kBlocks = EL == 16 ? 256 : 512;
+
 // Whole: each block takes whole (group, head)s, and nothing is left to join.
 template <typename T, int NC, int EL, bool Full, bool Beams, bool Whole>
 __global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const AttendArgs a, const Split w) {
@@ -356,7 +361,8 @@ __global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const Att
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, g = lane >> 4;
     const int heads = a.kv_heads * w.parts;
-    int64_t runs = gridDim.x, total = 0, before = 0, mine = 0, g0 = 0;
+    const int64_t run = blockIdx.x;
+    int64_t runs = 0, total = 0, before = 0, mine = 0, g0 = 0;
     if (!Whole) {
         // units of all groups: each thread sums some neighbours
         const int64_t per = (w.groups + kThreads - 1) / kThreads;
@@ -377,13 +383,12 @@ __global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const Att
         }
         before += upto - mine;
         total *= heads;
-        const int64_t rounds = total / (static_cast<int64_t>(gridDim.x) * kRunTiles);
-        runs *= rounds < 1 ? 1 : rounds < w.rounds ? rounds : w.rounds;
+        const int64_t rounds = total / (static_cast<int64_t>(kBlocks<EL>) * kRunTiles);
+        runs = kBlocks<EL> * (rounds < 1 ? 1 : rounds < w.rounds ? rounds : w.rounds);
         runs = total < runs ? total : runs;
-        for (int r = threadIdx.x; r < w.rounds; r += kThreads) w.joins[static_cast<int64_t>(r) * gridDim.x + blockIdx.x].first = -1;
-        __syncthreads();
+        if (threadIdx.x == 0) w.joins[run].first = -1;
+        if (run >= runs) return;
     }
-    for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
     int64_t gi, u, end;                             // group; unit of the whole row, and where the run ends
     int64_t units, head, v;                         // the group's units for a head, the head, unit within it
     if (Whole) {
@@ -508,7 +513,6 @@ __global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const Att
             if (u < end) units = units_of<Beams>(a, w, gi);
         }
     }
-    }
 }
 
 // The partial sums of one (group, head): the first run's second ones, and the others'
@@ -570,16 +574,15 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
     }
 }
 
-// Blocks of the split kernel: as many as are resident at once.
-template <int EL>
-constexpr int kBlocks = EL == 16 ? 256 : 512;
-
 // Rows of partial sums that the workspace holds: a run leaves two of each of its columns.
 constexpr int kSumRows = 32768;
 
-int most_rounds(int cols, int blocks) {
-    const int r = kSumRows / (2 * cols * blocks);
-    return r < 1 ? 1 : r < 8 ? r : 8;
+// Rounds of runs that a launch has blocks for: as many as the workspace holds the
+// sums of, and as the tiles could ask for if every sequence filled its table.
+int most_rounds(int cols, int blocks, int64_t tiles) {
+    const int64_t room = kSumRows / (2 * cols * blocks), asked = tiles / (static_cast<int64_t>(blocks) * kRunTiles);
+    const int64_t r = asked < room ? asked : room;
+    return r < 1 ? 1 : r < 8 ? static_cast<int>(r) : 8;
 }
 
 // Up to this many keys a sequence a block takes whole (group, head)s.
@@ -604,7 +607,7 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
     w.chunks = (a.beams + w.gb - 1) / w.gb;
     w.groups = a.n / a.beams * w.chunks;
     w.cols = w.parts > 1 ? kCols : w.gb * w.group;
-    w.rounds = most_rounds(w.cols, kBlocks<EL>);
+    w.rounds = most_rounds(w.cols, kBlocks<EL>, a.n * heads * ((static_cast<int64_t>(a.max_pages) * a.page + kTile - 1) / kTile));
     char* at = static_cast<char*>(workspace);
     w.o = reinterpret_cast<float*>(at);
     w.ml = reinterpret_cast<float*>(at += round256(static_cast<int64_t>(kSumRows) * a.d * 4));
@@ -615,9 +618,9 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
         w.shared = shared;
         const int64_t blocks = (w.groups + kWaves - 1) / kWaves;
         k_attend_shared<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kThreads, 0, stream>>>(a, w, shared);
-        k_attend<T, NC, EL, Full, true, false><<<kBlocks<EL>, kThreads, 0, stream>>>(a, w);
+        k_attend<T, NC, EL, Full, true, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
     } else {
-        k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL>, kThreads, 0, stream>>>(a, w);
+        k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
     }
     k_attend_join<T><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
     return hipGetLastError();
