@@ -7,9 +7,11 @@
 // each lane, a running maximum and sum of exponentials, and, one a lane, the
 // part's k best so far in order (within a row the logits alone order the
 // tokens). What is not above the last of them costs a comparison; what is, is
-// put in its place by a shift of the lanes behind it. A second launch joins a
-// request's parts: the sums in fp64, then the k best of the parts' candidates.
+// put in its place by a shift of the lanes behind it, or, where there are many,
+// sorted over the lanes and merged. A second launch joins a request's parts: the
+// sums in fp64, then the k best of the parts' candidates.
 
+#include "../../include/i8mm.h"
 #include "launch.h"
 
 #include "adapt_common.h"
@@ -49,6 +51,68 @@ __device__ __forceinline__ V least() {
     else return -INFINITY;
 }
 
+// The value of lane xor J: lane permutes within 16, swaps of rows beyond.
+template <int J>
+__device__ __forceinline__ unsigned other_bits(unsigned v, int lane) {
+    if constexpr (J == 1) return __builtin_amdgcn_update_dpp(0, v, 0xb1, 0xf, 0xf, true);
+    else if constexpr (J == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4e, 0xf, 0xf, true);
+    else if constexpr (J == 4)
+        return __builtin_amdgcn_update_dpp(0, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
+    else if constexpr (J == 8) return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true);
+    else if constexpr (J == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return lane & 16 ? p[0] : p[1];
+    } else {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return lane & 32 ? p[0] : p[1];
+    }
+}
+template <int J>
+__device__ __forceinline__ int other(int v, int lane) { return static_cast<int>(other_bits<J>(static_cast<unsigned>(v), lane)); }
+template <int J>
+__device__ __forceinline__ float other(float v, int lane) {
+    return __builtin_bit_cast(float, other_bits<J>(__builtin_bit_cast(unsigned, v), lane));
+}
+template <int J>
+__device__ __forceinline__ double other(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = other_bits<J>(static_cast<unsigned>(b), lane), hi = other_bits<J>(static_cast<unsigned>(b >> 32), lane);
+    return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+// The value of the lane before (lane 0: its own).
+__device__ __forceinline__ int previous(int v) { return __builtin_amdgcn_update_dpp(v, v, 0x138, 0xf, 0xf, false); }
+__device__ __forceinline__ float previous(float v) { return __builtin_bit_cast(float, previous(__builtin_bit_cast(int, v))); }
+__device__ __forceinline__ double previous(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = static_cast<uint32_t>(previous(static_cast<int>(b))), hi = static_cast<uint32_t>(previous(static_cast<int>(b >> 32)));
+    return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+// One step of a bitonic sort: of lanes l and l xor J the better pair goes to the lower
+// one, where `down`, else to the higher.
+template <int J, typename V>
+__device__ __forceinline__ void exchange(V& v, int& i, bool down, int lane) {
+    const V ov = other<J>(v, lane);
+    const int oi = other<J>(i, lane);
+    const bool mine = (v > ov) | ((v == ov) & (i < oi)), low = (lane & J) == 0;
+    if (mine != (low == down)) {
+        v = ov;
+        i = oi;
+    }
+}
+template <int J, typename V>
+__device__ __forceinline__ void bitonic_merge(V& v, int& i, bool down, int lane) {
+    exchange<J>(v, i, down, lane);
+    if constexpr (J > 1) bitonic_merge<J / 2>(v, i, down, lane);
+}
+// The wavefront's pairs in order, the best in lane 0.
+template <int N = kWave, typename V>
+__device__ __forceinline__ void sort_lanes(V& v, int& i, int lane) {
+    if constexpr (N > 2) sort_lanes<N / 2>(v, i, lane);
+    bitonic_merge<N / 2>(v, i, (lane & N) == 0, lane);
+}
+
 // The k <= 64 best (value, index) pairs seen by a wavefront, lane i the i-th.
 template <typename V>
 struct Best {
@@ -57,25 +121,46 @@ struct Best {
     V last = least<V>();                         // the k-th
     int last_index = kNone;
 
-    __device__ __forceinline__ bool wants(V v, int i) const { return v > last || (v == last && i < last_index); }
-    __device__ __forceinline__ void insert(V v, int i, int k, int lane) {
-        const uint64_t ahead = __ballot(value > v || (value == v && index < i));
-        const int at = __builtin_popcountll(ahead);
-        const V up = __shfl_up(value, 1, kWave);
-        const int up_index = __shfl_up(index, 1, kWave);
-        value = lane > at ? up : lane == at ? v : value;
-        index = lane > at ? up_index : lane == at ? i : index;
+    __device__ __forceinline__ bool wants(V v, int i) const { return (v > last) | ((v == last) & (i < last_index)); }
+    __device__ __forceinline__ void note_last(int k) {
         last = lane_value(value, k - 1);
         last_index = __builtin_amdgcn_readlane(index, k - 1);
     }
-    // Each lane offers one pair.
-    __device__ __forceinline__ void offer(V v, int i, bool real, int k, int lane) {
-        uint64_t left = __ballot(real && wants(v, i));
-        while (left) {
-            const int from = __builtin_ctzll(left);
-            insert(lane_value(v, from), __builtin_amdgcn_readlane(i, from), k, lane);
-            left = __ballot(real && wants(v, i)) & left & (left - 1);
+    // Behind the better ones; the others move up a lane. (note_last() is still to be called.)
+    __device__ __forceinline__ void insert(V v, int i, int lane) {
+        const int at = __builtin_popcountll(__ballot((value > v) | ((value == v) & (index < i))));
+        const V up = previous(value);
+        const int up_index = previous(index);
+        value = lane > at ? up : lane == at ? v : value;
+        index = lane > at ? up_index : lane == at ? i : index;
+    }
+    // A list in order, the i-th best in lane 63 - i: the better of each lane's two are
+    // the 64 best, falling and rising, which a bitonic merge puts in order.
+    __device__ __forceinline__ void merge_reversed(V v, int i, int k, int lane) {
+        if ((v > value) | ((v == value) & (i < index))) {
+            value = v;
+            index = i;
         }
+        bitonic_merge<kWave / 2>(value, index, true, lane);
+        note_last(k);
+    }
+    // Each lane offers one pair. A few are put in one after the other (some 150 cycles
+    // each); many are sorted and merged (some 1000 to 2500 in all).
+    __device__ __forceinline__ void offer(V v, int i, bool real, int k, int lane) {
+        uint64_t left = __ballot(real & wants(v, i));
+        if (__builtin_popcountll(left) > 8) {
+            V sv = real ? v : least<V>();
+            int si = real ? i : kNone;
+            sort_lanes(sv, si, lane);
+            merge_reversed(__shfl(sv, kWave - 1 - lane, kWave), __shfl(si, kWave - 1 - lane, kWave), k, lane);
+            return;
+        }
+        if (!left) return;
+        for (; left; left &= left - 1) {
+            const int from = __builtin_ctzll(left);
+            insert(lane_value(v, from), __builtin_amdgcn_readlane(i, from), lane);
+        }
+        note_last(k);
     }
 };
 
@@ -92,25 +177,32 @@ struct SelectScratch {
     int32_t* token;                              // [rows][parts][k]
 };
 
-// Part of a row: a running maximum and sum (of powers of 2 of the logits times
-// log2 e), and the k largest logits.
+// Part of a row, a quarter of it a wavefront: a running maximum and sum of
+// exponentials, and the k largest logits.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, const SelectScratch w, int parts, int part_len) {
+__global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, const SelectScratch w, int parts, int quarter) {
+    __shared__ float s_value[kWaves][kWave], s_m[kWaves], s_l[kWaves];
+    __shared__ volatile float s_floor[kWaves];   // the k-th best of each wavefront so far: what lies below is not wanted
+    __shared__ int s_index[kWaves][kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t items = a.n * a.beams * parts;
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + wave; item < items;
-         item += static_cast<int64_t>(gridDim.x) * kWaves) {
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t row = item / parts;
         const int part = static_cast<int>(item - row * parts);
         const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-        const int from = part * part_len, to = from + part_len < a.vocab ? from + part_len : a.vocab;
+        const int64_t first = (static_cast<int64_t>(part) * kWaves + wave) * quarter;
+        const int from = static_cast<int>(first < a.vocab ? first : a.vocab);
+        const int to = a.vocab - from < quarter ? a.vocab : from + quarter;
+        if (lane == 0) s_floor[wave] = -INFINITY;
+        __syncthreads();
         Best<float> best;
         float m = -INFINITY, l = 0.0f;
+        Eight<T> e, next;
+        if (from < to) e.load(x + from + 8 * lane, to - from - 8 * lane);
         for (int v0 = from; v0 < to; v0 += kStep) {
             const int v = v0 + 8 * lane;
+            if (v0 + kStep < to) next.load(x + v + kStep, to - v - kStep);
             float f[8];
-            Eight<T> e;
-            e.load(x + v, to - v);
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -124,21 +216,50 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
             for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((f[i] - off) * kLog2e);
             l = __builtin_fmaf(l, m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - off) * kLog2e), s);
             m = up;
-            if (__any(v < to && best.wants(most, v))) {
+            float floor = fmaxf(fmaxf(s_floor[0], s_floor[1]), fmaxf(s_floor[2], s_floor[3]));
+            if (__any((v < to) & (most >= floor) & best.wants(most, v))) {
+                // In the first step all are wanted; but the k best are not below the k-th of the lanes' largest.
+                if (v0 == from) {
+                    float sorted = most;
+                    int any = lane;
+                    sort_lanes(sorted, any, lane);
+                    floor = fmaxf(floor, lane_float(sorted, a.k - 1));
+                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) best.offer(f[i], v + i, v + i < to, a.k, lane);
+                for (int i = 0; i < 8; ++i) best.offer(f[i], v + i, (v + i < to) & (f[i] >= floor), a.k, lane);
+                if (lane == 0) s_floor[wave] = best.last;
             }
+            e = next;
         }
         const float top = wave_max_f(m);
         l = wave_sum(m == -INFINITY ? l : l * __builtin_amdgcn_exp2f((m - top) * kLog2e));
         if (lane == 0) {
-            w.most[item] = top;
-            w.sum[item] = l;
+            s_m[wave] = top;
+            s_l[wave] = l;
         }
-        if (lane < a.k) {
-            w.value[item * a.k + lane] = best.value;
-            w.token[item * a.k + lane] = best.index;
+        s_value[wave][lane] = best.value;
+        s_index[wave][lane] = best.index;
+        __syncthreads();
+        if (wave == 0) {
+            float all = s_m[0], sum = 0.0f;
+#pragma unroll
+            for (int o = 1; o < kWaves; ++o) {
+                all = fmaxf(all, s_m[o]);
+                best.merge_reversed(s_value[o][kWave - 1 - lane], s_index[o][kWave - 1 - lane], a.k, lane);
+            }
+#pragma unroll
+            for (int o = 0; o < kWaves; ++o)
+                sum += s_m[o] == -INFINITY ? s_l[o] : s_l[o] * __builtin_amdgcn_exp2f((s_m[o] - all) * kLog2e);
+            if (lane == 0) {
+                w.most[item] = all;
+                w.sum[item] = sum;
+            }
+            if (lane < a.k) {
+                w.value[item * a.k + lane] = best.value;
+                w.token[item * a.k + lane] = best.index;
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -146,27 +267,31 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
 __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, const SelectScratch w, int parts) {
     __shared__ double s_value[kWaves][kWave];
     __shared__ int s_index[kWaves][kWave];
+    static_assert(I8MM_BEAM_MAX * 4 <= kThreads && I8MM_BEAM_MAX <= kWave, "four lanes a beam, a lane a continuation");
     __shared__ double s_lse[kWave];              // of each beam; NaN: the beam leaves nothing
     __shared__ int s_parent[kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t b = blockIdx.x; b < a.n; b += gridDim.x) {
         const int64_t row0 = b * a.beams;
-        for (int i = wave; i < a.beams; i += kWaves) {
-            const float* most = w.most + (row0 + i) * parts;
-            const float* sum = w.sum + (row0 + i) * parts;
+        {
+            // four lanes a beam
+            const int i = threadIdx.x >> 2;
+            const bool there = i < a.beams;
+            const float* most = w.most + (row0 + (there ? i : 0)) * parts;
+            const float* sum = w.sum + (row0 + (there ? i : 0)) * parts;
             float top = -INFINITY;
-            for (int p = lane; p < parts; p += kWave) top = fmaxf(top, most[p]);
-            top = wave_max_f(top);
+            for (int p = threadIdx.x & 3; p < parts; p += 4) top = fmaxf(top, most[p]);
+            top = fmaxf(top, other<1>(top, lane));
+            top = fmaxf(top, other<2>(top, lane));
             double l = 0.0;
-            for (int p = lane; p < parts; p += kWave) {
-                const double by = most[p] == -INFINITY ? 0.0 : exp(static_cast<double>(most[p]) - top);
-                l += sum[p] * by;
+            for (int p = threadIdx.x & 3; p < parts; p += 4)
+                l += sum[p] * (most[p] == -INFINITY ? 0.0 : exp(static_cast<double>(most[p]) - top));
+            l += other<1>(l, lane);
+            l += other<2>(l, lane);
+            if (there && (threadIdx.x & 3) == 0) {
+                const double lse = top + log(l), score = a.scores[row0 + i];
+                s_lse[i] = (lse - lse) + (score - score) == 0.0 ? lse : NAN;
             }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, kWave);
-            const double score = a.scores[row0 + i];
-            const double lse = top + log(l);
-            if (lane == 0) s_lse[i] = (lse - lse) + (score - score) == 0.0 ? lse : NAN;
         }
         __syncthreads();
         Best<double> best;
@@ -196,9 +321,11 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
         __syncthreads();
         if (wave == 0) {
             for (int o = 1; o < kWaves; ++o)
-                best.offer(s_value[o][lane], s_index[o][lane], lane < a.k && s_index[o][lane] != kNone, a.k, lane);
+                best.merge_reversed(s_value[o][kWave - 1 - lane], s_index[o][kWave - 1 - lane], a.k, lane);
             if (lane < a.k) {
-                const int beam = best.index / a.vocab, v = best.index - beam * a.vocab;
+                // (in range whatever the workspace holds, should calls that overlap share one)
+                const int rank = best.index / a.vocab, beam = rank < a.beams ? rank : a.beams - 1;
+                const int v = best.index - beam * a.vocab;
                 a.scores_out[b * a.k + lane] = static_cast<float>(best.value);
                 a.parents[b * a.k + lane] = static_cast<int>(row0 + beam);
                 a.tokens[b * a.k + lane] = v;
@@ -208,20 +335,50 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
         }
         __syncthreads();
         if (a.history_out) {
-            for (int i = wave; i < a.k; i += kWaves) {
-                const int32_t* in = a.history + (row0 + s_parent[i]) * a.ldh;
-                int32_t* out = a.history_out + (b * a.k + i) * a.ldho;
-                for (int64_t t = lane; t < a.T; t += kWave) out[t] = in[t];
+            // four tokens a thread and four times that in flight
+            const int64_t quads = (a.T + 3) / 4, pieces = quads * a.k;
+            for (int64_t p0 = threadIdx.x; p0 < pieces; p0 += 4 * kThreads) {
+                v4i t[4];
+                int32_t* to[4];
+                int n[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t p = p0 + q * kThreads;
+                    n[q] = 0;
+                    if (p >= pieces) continue;
+                    const int i = static_cast<int>(p / quads);
+                    const int64_t at = 4 * (p - i * quads);
+                    const int32_t* in = a.history + (row0 + s_parent[i]) * a.ldh + at;
+                    to[q] = a.history_out + (b * a.k + i) * a.ldho + at;
+                    n[q] = a.T - at < 4 ? static_cast<int>(a.T - at) : 4;
+                    if (n[q] == 4) {
+                        __builtin_memcpy(&t[q], in, 16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (e < n[q]) t[q][e] = in[e];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (n[q] == 4) {
+                        __builtin_memcpy(to[q], &t[q], 16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (e < n[q]) to[q][e] = t[q][e];
+                    }
+                }
             }
         }
         __syncthreads();
     }
 }
 
-// Parts of a row: as many as fill the chip four wavefronts to a SIMD, each of
-// four steps at least.
+// Parts of a row: as many as fill the chip with four blocks a CU, of a step a wavefront
+// at least.
 int parts_of(int64_t rows, int vocab) {
-    const int64_t fill = 4096 / (rows < 1 ? 1 : rows < 4096 ? rows : 4096), most = (vocab + 4 * kStep - 1) / (4 * kStep);
+    const int64_t fill = 1024 / (rows < 1 ? 1 : rows < 1024 ? rows : 1024), most = (vocab + kWaves * kStep - 1) / (kWaves * kStep);
     return static_cast<int>(fill < most ? fill : most);
 }
 
@@ -238,7 +395,8 @@ hipError_t launch_beam_select(const SelectArgs& a, void* workspace, hipStream_t 
     if (a.n == 0) return hipSuccess;
     const int64_t rows = a.n * a.beams;
     const int parts = parts_of(rows, a.vocab);
-    const int part_len = (a.vocab + parts * kStep - 1) / (parts * kStep) * kStep;
+    const int64_t steps = static_cast<int64_t>(parts) * kWaves * kStep;
+    const int quarter = static_cast<int>((a.vocab + steps - 1) / steps * kStep);
     const int64_t lists = rows * parts;
     char* at = static_cast<char*>(workspace);
     SelectScratch w;
@@ -246,11 +404,10 @@ hipError_t launch_beam_select(const SelectArgs& a, void* workspace, hipStream_t 
     w.sum = reinterpret_cast<float*>(at += round256(4 * lists));
     w.value = reinterpret_cast<float*>(at += round256(4 * lists));
     w.token = reinterpret_cast<int32_t*>(at + round256(4 * lists * a.k));
-    const int64_t blocks = (lists + kWaves - 1) / kWaves;
-    const unsigned grid = static_cast<unsigned>(blocks < 65536 ? blocks : 65536);
-    if (a.type == Dtype::F16) k_select_scan<_Float16><<<grid, kThreads, 0, stream>>>(a, w, parts, part_len);
-    else if (a.type == Dtype::BF16) k_select_scan<__bf16><<<grid, kThreads, 0, stream>>>(a, w, parts, part_len);
-    else k_select_scan<float><<<grid, kThreads, 0, stream>>>(a, w, parts, part_len);
+    const unsigned grid = static_cast<unsigned>(lists < 65536 ? lists : 65536);
+    if (a.type == Dtype::F16) k_select_scan<_Float16><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
+    else if (a.type == Dtype::BF16) k_select_scan<__bf16><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
+    else k_select_scan<float><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
     k_select_join<<<static_cast<unsigned>(a.n < 65536 ? a.n : 65536), kThreads, 0, stream>>>(a, w, parts);
     return hipGetLastError();
 }
