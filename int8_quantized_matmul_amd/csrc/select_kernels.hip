@@ -113,6 +113,19 @@ __device__ __forceinline__ void sort_lanes(V& v, int& i, int lane) {
     bitonic_merge<N / 2>(v, i, (lane & N) == 0, lane);
 }
 
+// The wavefront's values in order, the largest in lane 0.
+template <int J>
+__device__ __forceinline__ void value_merge(float& v, bool down, int lane) {
+    const float o = other<J>(v, lane);
+    v = ((lane & J) == 0) == down ? fmaxf(v, o) : fminf(v, o);
+    if constexpr (J > 1) value_merge<J / 2>(v, down, lane);
+}
+template <int N = kWave>
+__device__ __forceinline__ void sort_values(float& v, int lane) {
+    if constexpr (N > 2) sort_values<N / 2>(v, lane);
+    value_merge<N / 2>(v, (lane & N) == 0, lane);
+}
+
 // The k <= 64 best (value, index) pairs seen by a wavefront, lane i the i-th.
 template <typename V>
 struct Best {
@@ -144,18 +157,17 @@ struct Best {
         bitonic_merge<kWave / 2>(value, index, true, lane);
         note_last(k);
     }
-    // Each lane offers one pair. A few are put in one after the other (some 150 cycles
-    // each); many are sorted and merged (some 1000 to 2500 in all).
-    __device__ __forceinline__ void offer(V v, int i, bool real, int k, int lane) {
-        uint64_t left = __ballot(real & wants(v, i));
+    // The lanes of `left` offer one pair each; some may be behind the k-th by now. A few
+    // are put in one after the other; many are sorted and merged.
+    __device__ __forceinline__ void offer(V v, int i, uint64_t left, int k, int lane) {
         if (__builtin_popcountll(left) > 8) {
+            const bool real = left >> lane & 1;
             V sv = real ? v : least<V>();
             int si = real ? i : kNone;
             sort_lanes(sv, si, lane);
             merge_reversed(__shfl(sv, kWave - 1 - lane, kWave), __shfl(si, kWave - 1 - lane, kWave), k, lane);
             return;
         }
-        if (!left) return;
         for (; left; left &= left - 1) {
             const int from = __builtin_ctzll(left);
             insert(lane_value(v, from), __builtin_amdgcn_readlane(i, from), lane);
@@ -163,6 +175,13 @@ struct Best {
         note_last(k);
     }
 };
+
+// The next fp32 number above v (v itself if there is none).
+__device__ __forceinline__ float above(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    const int up = v == 0.0f ? 1 : b < 0 ? b - 1 : b + (v < INFINITY);
+    return __builtin_bit_cast(float, up);
+}
 
 __device__ __forceinline__ float wave_max_f(float v) {
 #pragma unroll
@@ -216,17 +235,22 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
             for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((f[i] - off) * kLog2e);
             l = __builtin_fmaf(l, m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - off) * kLog2e), s);
             m = up;
-            float floor = fmaxf(fmaxf(s_floor[0], s_floor[1]), fmaxf(s_floor[2], s_floor[3]));
-            if (__any((v < to) & (most >= floor) & best.wants(most, v))) {
-                // In the first step all are wanted; but the k best are not below the k-th of the lanes' largest.
+            // What is below the bar is not wanted: nothing below another wavefront's k-th; of what this one
+            // has k of, nothing up to the k-th (a later token loses a tie).
+            const float floor = fmaxf(fmaxf(s_floor[0], s_floor[1]), fmaxf(s_floor[2], s_floor[3]));
+            float bar = best.last_index == kNone ? floor : fmaxf(floor, above(best.last));
+            if (__any(most >= bar)) {
                 if (v0 == from) {
+                    // in the first step, nothing below the k-th of the lanes' largest
                     float sorted = most;
-                    int any = lane;
-                    sort_lanes(sorted, any, lane);
-                    floor = fmaxf(floor, lane_float(sorted, a.k - 1));
+                    sort_values(sorted, lane);
+                    bar = fmaxf(bar, lane_float(sorted, a.k - 1));
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) best.offer(f[i], v + i, (v + i < to) & (f[i] >= floor), a.k, lane);
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t left = __ballot((f[i] >= bar) & (v + i < to));
+                    if (left) best.offer(f[i], v + i, left, a.k, lane);
+                }
                 if (lane == 0) s_floor[wave] = best.last;
             }
             e = next;
@@ -274,21 +298,20 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
     for (int64_t b = blockIdx.x; b < a.n; b += gridDim.x) {
         const int64_t row0 = b * a.beams;
         {
-            // four lanes a beam
-            const int i = threadIdx.x >> 2;
+            // as many lanes a beam as there are, up to a wavefront
+            const int lanes = a.beams <= 4 ? 64 : a.beams <= 8 ? 32 : a.beams <= 16 ? 16 : a.beams <= 32 ? 8 : 4;
+            const int i = threadIdx.x / lanes, p0 = threadIdx.x & (lanes - 1);
             const bool there = i < a.beams;
             const float* most = w.most + (row0 + (there ? i : 0)) * parts;
             const float* sum = w.sum + (row0 + (there ? i : 0)) * parts;
             float top = -INFINITY;
-            for (int p = threadIdx.x & 3; p < parts; p += 4) top = fmaxf(top, most[p]);
-            top = fmaxf(top, other<1>(top, lane));
-            top = fmaxf(top, other<2>(top, lane));
+            for (int p = p0; p < parts; p += lanes) top = fmaxf(top, most[p]);
+            for (int off = lanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
             double l = 0.0;
-            for (int p = threadIdx.x & 3; p < parts; p += 4)
+            for (int p = p0; p < parts; p += lanes)
                 l += sum[p] * (most[p] == -INFINITY ? 0.0 : exp(static_cast<double>(most[p]) - top));
-            l += other<1>(l, lane);
-            l += other<2>(l, lane);
-            if (there && (threadIdx.x & 3) == 0) {
+            for (int off = lanes / 2; off > 0; off >>= 1) l += __shfl_xor(l, off, kWave);
+            if (there && p0 == 0) {
                 const double lse = top + log(l), score = a.scores[row0 + i];
                 s_lse[i] = (lse - lse) + (score - score) == 0.0 ? lse : NAN;
             }
@@ -314,7 +337,9 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
                     v = rank < a.vocab ? rank : kNone;   // nothing to choose by: the lowest tokens, with no weight
                 }
             }
-            best.offer(t, v == kNone ? kNone : beam * a.vocab + v, v != kNone, a.k, lane);
+            const int at = v == kNone ? kNone : beam * a.vocab + v;
+            const uint64_t left = __ballot((v != kNone) & best.wants(t, at));
+            if (left) best.offer(t, at, left, a.k, lane);
         }
         s_value[wave][lane] = best.value;
         s_index[wave][lane] = best.index;
