@@ -689,7 +689,8 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
 /* Limits: pages of a pool, tokens of a page, pages of a sequence (and max_pages
  * * page < 2^31 - 4096), sequences of a call, features of a head (a multiple of
  * 8), rows of an append, beams of a request and continuations kept of one, tokens
- * of the vocabulary. */
+ * of the vocabulary; and the positions of a sequence up to which the attention
+ * takes no workspace. */
 #define I8MM_CACHE_MAX_PAGES 16777216
 #define I8MM_CACHE_MAX_PAGE 4096
 #define I8MM_CACHE_MAX_ROW 1048576
@@ -698,6 +699,7 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
 #define I8MM_CACHE_MAX_APPEND 16777216
 #define I8MM_BEAM_MAX 64
 #define I8MM_BEAM_MAX_VOCAB 16777216
+#define I8MM_ATTENTION_WHOLE_KEYS 512
 
 /*
  * Appends rows to their sequences' pages: for each i < s, with q = seq[i]
@@ -796,7 +798,8 @@ size_t i8mm_decode_attention_workspace_bytes(int64_t n, int64_t heads, int64_t k
  * many neighbours, which divides n; pages that a group's tables share are read
  * once for the group. It changes the speed alone; 1 is always right. workspace:
  * i8mm_decode_attention_workspace_bytes(...) bytes, 256-byte aligned, contents
- * unspecified before and after.
+ * unspecified before and after; NULL is accepted if max_pages * page is at most
+ * I8MM_ATTENTION_WHOLE_KEYS.
  * What lies behind a sequence's last token never reaches it, NaN and infinity
  * included.
  */

@@ -91,6 +91,8 @@ LORA_MAX_RANK = _native.header_define("I8MM_LORA_MAX_RANK")
 
 # Most beams of a request, and continuations kept of one (I8MM_BEAM_MAX).
 BEAM_MAX = _native.header_define("I8MM_BEAM_MAX")
+# Up to this many positions a sequence decode_attention takes no workspace.
+_WHOLE_KEYS = _native.header_define("I8MM_ATTENTION_WHOLE_KEYS")
 
 
 class I8MMError(RuntimeError):
@@ -900,15 +902,14 @@ def _pages(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -
                          f"(got {t.dtype} of shape {tuple(t.shape)} on {t.device})")
     if not t.is_contiguous() and not (t.shape[0] and t[0].is_contiguous()):
         raise ValueError(f"{name} must hold each page without gaps (strides {t.stride()})")
-    dense = t.shape[1] * t.shape[2] * t.shape[3]
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else dense
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.numel()    # the stride of a single page says nothing
 
 
 def _pool_table(pools: Sequence[torch.Tensor], n_pages: int, device: int):
     """(pointers, bytes of a page, bytes between pages) of tensors [n_pages, ...], as host arrays."""
     at, size, step = array.array("Q"), array.array("q"), array.array("q")
     for t in pools:
-        if t.get_device() != device or t.dim() < 1 or t.shape[0] != n_pages or not t[0].is_contiguous():
+        if t.get_device() != device or t.dim() < 1 or t.shape[0] != n_pages or not (t.is_contiguous() or t[0].is_contiguous()):
             raise ValueError(f"pools must be tensors of {n_pages} pages without gaps in them on the current GPU, cuda:{device}")
         e = t.element_size()
         at.append(t.data_ptr())
@@ -1061,10 +1062,13 @@ def decode_attention(q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tens
         y, ldo = _matrix(out, "out", q.dtype, (n, w), dev)
     lse = _new_or(lse, "lse", q, (n, heads), torch.float32, dev)
     sl = None if slopes is None else _dense(slopes, "slopes", torch.float32, (heads,), dev)
-    workspace = _scratch(decode_attention_workspace(n, heads, kv, d), "decode_attention", workspace, q.device)
+    ws = None
+    if M * page > _WHOLE_KEYS or workspace is not None:
+        workspace = _scratch(decode_attention_workspace(n, heads, kv, d), "decode_attention", workspace, q.device)
+        ws = workspace.data_ptr()
     st = _lib.i8mm_decode_attention(x, ldq, _DTYPES[q.dtype], n, heads, kv, d, k, sk, v, sv, P, page, t, ldt, M,
                                     _ints(lens, "lens", n, dev), beams, d ** -0.5 if scale is None else scale, sl, y, ldo,
-                                    lse.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
+                                    lse.data_ptr(), ws, _raw_stream(dev))
     _check(st, "decode_attention")
     return out, lse
 

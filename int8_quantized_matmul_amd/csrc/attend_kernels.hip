@@ -19,6 +19,7 @@
 // even so (24 instructions of 16 cycles for 16 KB of cache), since the
 // cache's bytes are what bounds the kernel.
 
+#include "../../include/i8mm.h"
 #include "launch.h"
 
 #include "adapt_common.h"
@@ -356,12 +357,12 @@ constexpr int kBlocks = EL == 16 ? 256 : 512;
 
 // Whole: each block takes whole (group, head)s, and nothing is left to join.
 template <typename T, int NC, int EL, bool Full, bool Beams, bool Whole>
-__global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const AttendArgs a, const Split w) {
+__global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const AttendArgs a, const Split w, int64_t run0) {
     __shared__ Attend<NC, EL> s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, g = lane >> 4;
     const int heads = a.kv_heads * w.parts;
-    const int64_t run = blockIdx.x;
+    const int64_t run = run0 + blockIdx.x;
     int64_t runs = 0, total = 0, before = 0, mine = 0, g0 = 0;
     if (!Whole) {
         // units of all groups: each thread sums some neighbours
@@ -585,8 +586,9 @@ int most_rounds(int cols, int blocks, int64_t tiles) {
     return r < 1 ? 1 : r < 8 ? static_cast<int>(r) : 8;
 }
 
-// Up to this many keys a sequence a block takes whole (group, head)s.
-constexpr int kWholeKeys = 4 * kTile;
+// Up to this many keys a sequence a block takes whole (group, head)s: one launch, and
+// no workspace.
+constexpr int kWholeKeys = I8MM_ATTENTION_WHOLE_KEYS;
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -595,13 +597,17 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
     w.group = a.heads / a.kv_heads;
     w.parts = (w.group + kCols - 1) / kCols;
     const int heads = a.kv_heads * w.parts;
-    if (static_cast<int64_t>(a.max_pages) * a.page <= kWholeKeys && a.n * heads < (int64_t(1) << 23)) {
+    if (static_cast<int64_t>(a.max_pages) * a.page <= kWholeKeys) {
         w.groups = a.n;
         w.gb = w.chunks = 1;
         AttendArgs one = a;
         one.beams = 1;
-        k_attend<T, NC, EL, Full, false, true><<<static_cast<unsigned>(a.n * heads), kThreads, 0, stream>>>(one, w);
-        return hipGetLastError();
+        // in runs of blocks that one grid has threads for
+        const int64_t items = a.n * heads;
+        return for_row_runs(items, kGridThreads / kThreads, [&](int64_t first, int64_t count) {
+            k_attend<T, NC, EL, Full, false, true><<<static_cast<unsigned>(count), kThreads, 0, stream>>>(one, w, first);
+            return hipGetLastError();
+        });
     }
     w.gb = w.parts > 1 ? 1 : kCols / w.group < a.beams ? kCols / w.group : a.beams;
     w.chunks = (a.beams + w.gb - 1) / w.gb;
@@ -618,9 +624,9 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
         w.shared = shared;
         const int64_t blocks = (w.groups + kWaves - 1) / kWaves;
         k_attend_shared<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kThreads, 0, stream>>>(a, w, shared);
-        k_attend<T, NC, EL, Full, true, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
+        k_attend<T, NC, EL, Full, true, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w, 0);
     } else {
-        k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
+        k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w, 0);
     }
     k_attend_join<T><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
     return hipGetLastError();
