@@ -362,13 +362,14 @@ __device__ __forceinline__ void put(const AttendArgs& a, const Column& c, int i,
     if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum(m, l);
 }
 
-// Runs of the split kernel in multiples of the blocks that are resident at once.
+// Runs of the split kernel in multiples of the blocks that are resident at once; heads
+// of up to 64 features take twice as many to have as much in flight.
 template <int EL>
-constexpr int kBlocks = EL == 16 ? 256 : 512;
+constexpr int kBlocks = EL == 16 ? 256 : EL == 8 ? 512 : 1024;
 
 // Whole: each block takes whole (group, head)s, and nothing is left to join.
 template <typename T, int NC, int EL, bool Full, bool Beams, bool Whole>
-__global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const AttendArgs a, const Split w, int64_t run0) {
+__global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const AttendArgs a, const Split w, int64_t run0) {
     __shared__ Attend<NC, EL> s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, g = lane >> 4;
@@ -524,11 +525,14 @@ __global__ __launch_bounds__(kThreads, EL == 16 ? 1 : 2) void k_attend(const Att
 }
 
 // The partial sums of one (group, head): the first run's second ones, and the others'
-// first ones. Every 16 bytes of the result are summed by one thread, or, where there are
-// fewer of them than threads, by several that take the runs in turn.
+// first ones, kJoinCols columns a block. Every 16 bytes of the result are summed by one
+// thread, or, where there are fewer of them than threads, by several that take the runs
+// in turn.
+constexpr int kJoinCols = 4;
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, const Split w) {
-    __shared__ float s_m[kCols], s_l[kCols];
+    __shared__ float s_m[kJoinCols], s_l[kJoinCols];
     __shared__ v4f s_o[kThreads];
     const Split::Join j = w.joins[blockIdx.x];
     if (j.first < 0) return;
@@ -538,12 +542,13 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
     const int n = static_cast<int>(blockIdx.x) - j.first + 1;
     const auto slot = [&](int b) { return (static_cast<int64_t>(j.first + b) * 2 + (b == 0)) * w.cols; };
     const int lane = threadIdx.x & 63;
-    for (int c = threadIdx.x >> 6; c < cols; c += kWaves) {
+    const int col0 = static_cast<int>(blockIdx.y) * kJoinCols, mine = cols - col0 < kJoinCols ? cols - col0 : kJoinCols;
+    for (int c = threadIdx.x >> 6; c < mine; c += kWaves) {
         float m = -INFINITY, l = 0.0f;
-        for (int b = lane; b < n; b += kWave) m = fmaxf(m, w.ml[(slot(b) + c) * 2]);
+        for (int b = lane; b < n; b += kWave) m = fmaxf(m, w.ml[(slot(b) + col0 + c) * 2]);
         m = wave_max(m);
         for (int b = lane; b < n; b += kWave) {
-            const float* p = w.ml + (slot(b) + c) * 2;
+            const float* p = w.ml + (slot(b) + col0 + c) * 2;
             l += p[0] == -INFINITY ? p[1] : p[1] * __builtin_amdgcn_exp2f(p[0] - m);
         }
         l = wave_sum(l);
@@ -552,8 +557,9 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
             s_l[c] = l;
         }
     }
+    if (mine <= 0) return;
     __syncthreads();
-    const int quads = a.d / 4, all = cols * quads, sharers = all < kThreads ? kThreads / all : 1;
+    const int quads = a.d / 4, all = mine * quads, sharers = all < kThreads ? kThreads / all : 1;
     for (int k0 = 0; k0 < all; k0 += kThreads) {
         const int by = static_cast<int>(threadIdx.x) / all, k = sharers > 1 ? static_cast<int>(threadIdx.x) - by * all : k0 + static_cast<int>(threadIdx.x);
         const bool there = sharers > 1 ? by < sharers : k < all;
@@ -562,7 +568,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
         if (there) {
 #pragma unroll 4
             for (int b = sharers > 1 ? by : 0; b < n; b += sharers) {
-                const int64_t at = slot(b) + c;
+                const int64_t at = slot(b) + col0 + c;
                 const float m = w.ml[at * 2], f = m == -INFINITY ? (w.ml[at * 2 + 1] == 0.0f ? 0.0f : 1.0f)
                                                                    : __builtin_amdgcn_exp2f(m - s_m[c]);
                 o += *reinterpret_cast<const v4f*>(w.o + at * a.d + i) * f;
@@ -575,7 +581,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
                 for (int b = 1; b < sharers; ++b) o += s_o[b * all + k];
         }
         if (there && (sharers == 1 || by == 0)) {
-            const Column col = column_of(w, grp, kv, part, c);
+            const Column col = column_of(w, grp, kv, part, col0 + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) put<T>(a, col, i + e, o[e], s_m[c], s_l[c]);
         }
@@ -635,7 +641,7 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
     } else {
         k_attend<T, NC, EL, Full, false, false><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w, 0);
     }
-    k_attend_join<T><<<kBlocks<EL> * w.rounds, kThreads, 0, stream>>>(a, w);
+    k_attend_join<T><<<dim3(kBlocks<EL> * w.rounds, (w.cols + kJoinCols - 1) / kJoinCols), kThreads, 0, stream>>>(a, w);
     return hipGetLastError();
 }
 
