@@ -684,7 +684,9 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
  *   - A page number outside [0, n_pages) names no page: nothing is read from it
  *     or written to it, and its positions are left out.
  *   - refs [n_pages] int32: how many table entries (and whatever else a caller
- *     counts in) hold each page. A page is free if its count is 0 or less.
+ *     counts in) hold each page. A page is free if its count is 0 or less; a page
+ *     that a table holds but refs does not count may be taken, and its contents
+ *     are then lost.
  */
 /* Limits: pages of a pool, tokens of a page, pages of a sequence (and max_pages
  * * page < 2^31 - 4096), sequences of a call, features of a head (a multiple of

@@ -907,6 +907,8 @@ def _pages(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -
 
 def _pool_table(pools: Sequence[torch.Tensor], n_pages: int, device: int):
     """(pointers, bytes of a page, bytes between pages) of tensors [n_pages, ...], as host arrays."""
+    if n_pages == 0:
+        raise ValueError("refs must have a count for each of at least one page")
     at, size, step = array.array("Q"), array.array("q"), array.array("q")
     for t in pools:
         if t.get_device() != device or t.dim() < 1 or t.shape[0] != n_pages or not (t.is_contiguous() or t[0].is_contiguous()):
@@ -1051,7 +1053,9 @@ def decode_attention(q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tens
     v, sv = _pages(V_pages, "V_pages", q.dtype, K_pages.shape, dev)
     P, kv, page, d = K_pages.shape
     n, w = q.shape
-    heads = w // d if d else 0
+    if d == 0:
+        raise ValueError("K_pages must have heads of at least 8 features (got 0)")
+    heads = w // d
     x, ldq = _matrix(q, "q", q.dtype, (n, heads * d), dev)
     M = tables.shape[1]
     t, ldt = _matrix(tables, "tables", torch.int32, (n, M), dev)

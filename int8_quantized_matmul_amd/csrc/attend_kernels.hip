@@ -49,18 +49,24 @@ constexpr int kCols = 16;                        // queries of one matrix instru
 constexpr int kRunTiles = 24;                    // tiles of a run, if there are enough for several runs a block
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-// The probabilities of the running maximum are 2^kShift, so that in fp16 those
-// down to 2^-29 of the largest keep all digits. The sum has the same factor.
-constexpr float kShift = 15.0f;
-
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 
+// kShift: the running maximum's probability is 2^kShift, and the sum has the same
+// factor. In fp16 15: probabilities keep all digits down to 2^-29 of the largest, and
+// sums of 2^31 values times 2^15 stay far below fp32's end. bf16 needs none, and with
+// values near fp32's end there is no room for one.
 template <typename T>
 struct Vec8;
 template <>
-struct Vec8<_Float16> { typedef v8h type; };
+struct Vec8<_Float16> {
+    typedef v8h type;
+    static constexpr float kShift = 15.0f;
+};
 template <>
-struct Vec8<__bf16> { typedef v8b type; };
+struct Vec8<__bf16> {
+    typedef v8b type;
+    static constexpr float kShift = 0.0f;
+};
 
 __device__ __forceinline__ v4f mma(v8h a, v8h b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ v4f mma(v8b a, v8b b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -181,7 +187,7 @@ __device__ __forceinline__ void add_step(Sums<EL>& sum, Step<NC, EL>& s, const Q
 #pragma unroll
         for (int e = 0; e < EL; ++e) sum.o[e] *= by;
     }
-    const float off = sum.m == -INFINITY ? 0.0f : sum.m - kShift;
+    const float off = sum.m == -INFINITY ? 0.0f : sum.m - Vec8<T>::kShift;
     vec w;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -310,7 +316,7 @@ struct Attend {
     int64_t at_group, at_units;
 };
 
-// Joins the wavefronts' sums; f(column, feature, o, m, l) for each, o and l relative to 2^(m - kShift).
+// Joins the wavefronts' sums; f(column, feature, o, m, l) for each, o and l relative to the maximum m.
 template <int NC, int EL, typename F>
 __device__ __forceinline__ void join_waves(Attend<NC, EL>& s, const Sums<EL>& sum, int cols, int d, int wave, int lane, F&& f) {
     const int x = lane & 15, g = lane >> 4;
@@ -343,7 +349,10 @@ __device__ __forceinline__ void join_waves(Attend<NC, EL>& s, const Sums<EL>& su
     __syncthreads();
 }
 
-__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_log2f(l) - kShift) * kLn2; }
+template <typename T>
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + __builtin_log2f(l) - Vec8<T>::kShift) * kLn2;
+}
 
 // Column c of a group's head: its sequence and head.
 struct Column {
@@ -359,7 +368,7 @@ __device__ __forceinline__ Column column_of(const Split& w, const Group& g, int 
 template <typename T>
 __device__ __forceinline__ void put(const AttendArgs& a, const Column& c, int i, float o, float m, float l) {
     static_cast<T*>(a.out)[c.seq * a.ldo + static_cast<int64_t>(c.head) * a.d + i] = static_cast<T>(l == 0.0f ? 0.0f : o / l);
-    if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum(m, l);
+    if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum<T>(m, l);
 }
 
 // Runs of the split kernel in multiples of the blocks that are resident at once; heads

@@ -129,7 +129,8 @@ def _many(rng, requests, beams, page, shared, mine, spare):
 
 
 @pytest.mark.parametrize("requests,beams,shared,mine,spare", [(300, 8, 11, 2, 20000), (1, 64, 500, 1, 3), (2500, 1, 0, 30, 100),
-                                                              (40, 4, 100, 3, 300), (1200, 2, 1, 1, 100000)])
+                                                              (40, 4, 100, 3, 300), (1200, 2, 1, 1, 100000),
+                                                              (128, 8, 20, 2, 28160), (128, 8, 20, 2, 28161), (205, 5, 9, 2, 50)])
 def test_fork_and_compact_of_many_sequences(requests, beams, shared, mine, spare):
     rng = np.random.default_rng(requests)
     page = 16

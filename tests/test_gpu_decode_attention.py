@@ -130,6 +130,18 @@ def test_small_weights_are_not_lost():
         _check(q, K, V, tables, [n], scale=1.0)
 
 
+def test_values_near_the_ends_of_the_types():
+    """bf16 values near fp32's end and near its smallest numbers, fp16's largest: nothing overflows or vanishes on the way."""
+    rng = np.random.default_rng(19)
+    lens, page, d = [3, 2, 700], 16, 64
+    tables, pages = paged(rng, lens, page)
+    for dtype, std in ((BF16, 2.0e37), (BF16, 1e-30), (F16, 9000.0), (F16, 1e-5)):
+        say(f"  launch: decode_attention, values of {std}, {dtype}")
+        n = lens if std < 1e30 else [3, 2, 5]             # the sum of a few such values is still a number of fp32
+        K, V = pool(rng, tables, n, pages, 2, page, d, dtype), pool(rng, tables, n, pages, 2, page, d, dtype, std=std)
+        _check(randn(rng, (3, 2 * d), dtype), K, V, tables, n)
+
+
 def test_values_that_are_not_finite():
     """A NaN or infinity among a sequence's tokens reaches the heads that read it alone, as the definition says; behind the
     last token (the pools are NaN there) and in other sequences it reaches nothing."""
