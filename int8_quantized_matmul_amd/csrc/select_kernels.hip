@@ -7,14 +7,16 @@
 // each lane, a running maximum and sum of exponentials, and, one a lane, the
 // part's k best so far in order (within a row the logits alone order the
 // tokens). What is not above the last of them costs a comparison; what is, is
-// put in its place by a shift of the lanes behind it, or, where there are many,
-// sorted over the lanes and merged. A second launch joins a request's parts: the
-// sums in fp64, then the k best of the parts' candidates.
+// put in its place by a shift of the lanes behind it. A second launch joins a
+// request's parts: the sums in fp64, then the k best of the parts' candidates,
+// which are sorted over the lanes and merged where they are many.
 
 #include "../../include/i8mm.h"
 #include "launch.h"
 
 #include "adapt_common.h"
+
+#include <type_traits>
 
 namespace i8mm {
 namespace {
@@ -157,8 +159,15 @@ struct Best {
         bitonic_merge<kWave / 2>(value, index, true, lane);
         note_last(k);
     }
-    // The lanes of `left` offer one pair each; some may be behind the k-th by now. A few
-    // are put in one after the other; many are sorted and merged.
+    // The lanes of `left` offer one pair each, which are put in one after the other.
+    __device__ __forceinline__ void offer_few(V v, int i, uint64_t left, int k, int lane) {
+        for (left &= __ballot(wants(v, i)); left; left &= left - 1) {
+            const int from = __builtin_ctzll(left);
+            insert(lane_value(v, from), __builtin_amdgcn_readlane(i, from), lane);
+        }
+        note_last(k);
+    }
+    // The same where they may be many: those are sorted and merged.
     __device__ __forceinline__ void offer(V v, int i, uint64_t left, int k, int lane) {
         if (__builtin_popcountll(left) > 8) {
             const bool real = left >> lane & 1;
@@ -166,13 +175,9 @@ struct Best {
             int si = real ? i : kNone;
             sort_lanes(sv, si, lane);
             merge_reversed(__shfl(sv, kWave - 1 - lane, kWave), __shfl(si, kWave - 1 - lane, kWave), k, lane);
-            return;
+        } else {
+            offer_few(v, i, left, k, lane);
         }
-        for (; left; left &= left - 1) {
-            const int from = __builtin_ctzll(left);
-            insert(lane_value(v, from), __builtin_amdgcn_readlane(i, from), lane);
-        }
-        note_last(k);
     }
 };
 
@@ -197,8 +202,13 @@ struct SelectScratch {
 };
 
 // Part of a row, a quarter of it a wavefront: a running maximum and sum of
-// exponentials, and the k largest logits.
-template <typename T>
+// exponentials, and the k largest logits. A wavefront takes `Steps` steps at once: the
+// more tokens are compared with one bar, the fewer are put in only to be pushed out
+// again. 64 x 8 beams over 50272 tokens in fp32, k = 16 (103 MB): 36 us with one
+// step, 34 with two or three, 40 with four (a longer program and a longer tail); 19
+// without the selection, which is what memory takes: each wavefront puts in some 50
+// tokens, one after the other.
+template <typename T, int Steps>
 __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, const SelectScratch w, int parts, int quarter) {
     __shared__ float s_value[kWaves][kWave], s_m[kWaves], s_l[kWaves];
     __shared__ volatile float s_floor[kWaves];   // the k-th best of each wavefront so far: what lies below is not wanted
@@ -216,23 +226,32 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
         __syncthreads();
         Best<float> best;
         float m = -INFINITY, l = 0.0f;
-        Eight<T> e, next;
-        if (from < to) e.load(x + from + 8 * lane, to - from - 8 * lane);
-        for (int v0 = from; v0 < to; v0 += kStep) {
+        Eight<T> next[Steps];
+#pragma unroll
+        for (int q = 0; q < Steps; ++q) next[q].load(x + from + q * kStep + 8 * lane, to - from - q * kStep - 8 * lane);
+        for (int v0 = from; v0 < to; v0 += Steps * kStep) {
             const int v = v0 + 8 * lane;
-            if (v0 + kStep < to) next.load(x + v + kStep, to - v - kStep);
-            float f[8];
+            float f[Steps][8];
             float most = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] = v + i < to ? e.at(i) : -INFINITY;
-                most = fmaxf(most, f[i]);
+            for (int q = 0; q < Steps; ++q)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[q][i] = v + q * kStep + i < to ? next[q].at(i) : -INFINITY;
+                    most = fmaxf(most, f[q][i]);
+                }
+            const int v1 = v + Steps * kStep;
+            if (v0 + Steps * kStep < to) {
+#pragma unroll
+                for (int q = 0; q < Steps; ++q) next[q].load(x + v1 + q * kStep, to - v1 - q * kStep);
             }
             const float up = fmaxf(m, most);
             const float off = up == -INFINITY ? 0.0f : up;
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((f[i] - off) * kLog2e);
+            for (int q = 0; q < Steps; ++q)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((f[q][i] - off) * kLog2e);
             l = __builtin_fmaf(l, m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - off) * kLog2e), s);
             m = up;
             // What is below the bar is not wanted: nothing below another wavefront's k-th; of what this one
@@ -241,19 +260,20 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
             float bar = best.last_index == kNone ? floor : fmaxf(floor, above(best.last));
             if (__any(most >= bar)) {
                 if (v0 == from) {
-                    // in the first step, nothing below the k-th of the lanes' largest
+                    // at first, nothing below the k-th of the lanes' largest
                     float sorted = most;
                     sort_values(sorted, lane);
                     bar = fmaxf(bar, lane_float(sorted, a.k - 1));
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint64_t left = __ballot((f[i] >= bar) & (v + i < to));
-                    if (left) best.offer(f[i], v + i, left, a.k, lane);
-                }
+                for (int q = 0; q < Steps; ++q)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint64_t left = __ballot((f[q][i] >= bar) & (v + q * kStep + i < to));
+                        if (left) best.offer_few(f[q][i], v + q * kStep + i, left, a.k, lane);
+                    }
                 if (lane == 0) s_floor[wave] = best.last;
             }
-            e = next;
         }
         const float top = wave_max_f(m);
         l = wave_sum(m == -INFINITY ? l : l * __builtin_amdgcn_exp2f((m - top) * kLog2e));
@@ -430,9 +450,15 @@ hipError_t launch_beam_select(const SelectArgs& a, void* workspace, hipStream_t 
     w.value = reinterpret_cast<float*>(at += round256(4 * lists));
     w.token = reinterpret_cast<int32_t*>(at + round256(4 * lists * a.k));
     const unsigned grid = static_cast<unsigned>(lists < 65536 ? lists : 65536);
-    if (a.type == Dtype::F16) k_select_scan<_Float16><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
-    else if (a.type == Dtype::BF16) k_select_scan<__bf16><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
-    else k_select_scan<float><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
+    // a wavefront with a step or two takes them one at a time
+    const auto scan = [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        if (quarter <= 2 * kStep) k_select_scan<T, 1><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
+        else k_select_scan<T, 2><<<grid, kThreads, 0, stream>>>(a, w, parts, quarter);
+    };
+    if (a.type == Dtype::F16) scan(static_cast<_Float16*>(nullptr));
+    else if (a.type == Dtype::BF16) scan(static_cast<__bf16*>(nullptr));
+    else scan(static_cast<float*>(nullptr));
     k_select_join<<<static_cast<unsigned>(a.n < 65536 ? a.n : 65536), kThreads, 0, stream>>>(a, w, parts);
     return hipGetLastError();
 }
