@@ -983,10 +983,15 @@ def cache_fork(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     at, size, step = _pool_table(pools, P, dev)
     if tables_out is None:
         tables_out = tables.new_empty((m, M))
-    to, ldto = _matrix(tables_out, "tables_out", torch.int32, (m, M), dev)
-    lens_out = _new_or(lens_out, "lens_out", lens, (m,), torch.int32, dev)
-    refs_out = _new_or(refs_out, "refs_out", refs, (P,), torch.int32, dev)
-    state = refs.new_empty(4)
+        to, ldto = tables_out.data_ptr(), M
+    else:
+        to, ldto = _matrix(tables_out, "tables_out", torch.int32, (m, M), dev)
+    if lens_out is None and refs_out is None:            # small parts of one allocation
+        refs_out, lens_out, state = refs.new_empty(P + m + 4).split((P, m, 4))
+    else:
+        lens_out = _new_or(lens_out, "lens_out", lens, (m,), torch.int32, dev)
+        refs_out = _new_or(refs_out, "refs_out", refs, (P,), torch.int32, dev)
+        state = refs.new_empty(4)
     workspace = _scratch(cache_fork_workspace(n, m, P), "cache_fork", workspace, tables.device)
     st = _lib.i8mm_cache_fork(t, ldt, l, r, n, M, P, page, p, g, m, to, ldto, lens_out.data_ptr(), refs_out.data_ptr(),
                               state.data_ptr(), at.buffer_info()[0], size.buffer_info()[0], step.buffer_info()[0], len(at),
@@ -1018,9 +1023,14 @@ def cache_compact(tables: torch.Tensor, refs: torch.Tensor, pools: Sequence[torc
     at, size, step = _pool_table(pools, P, dev)
     if tables_out is None:
         tables_out = tables.new_empty((n, M))
-    to, ldto = _matrix(tables_out, "tables_out", torch.int32, (n, M), dev)
-    refs_out = _new_or(refs_out, "refs_out", refs, (P,), torch.int32, dev)
-    moved, state = refs.new_empty(P), refs.new_empty(2)
+        to, ldto = tables_out.data_ptr(), M
+    else:
+        to, ldto = _matrix(tables_out, "tables_out", torch.int32, (n, M), dev)
+    if refs_out is None:                                 # small parts of one allocation
+        refs_out, moved, state = refs.new_empty(2 * P + 2).split((P, P, 2))
+    else:
+        _dense(refs_out, "refs_out", torch.int32, (P,), dev)
+        moved, state = refs.new_empty(P + 2).split((P, 2))
     workspace = _scratch(cache_compact_workspace(P), "cache_compact", workspace, tables.device)
     st = _lib.i8mm_cache_compact(t, ldt, n, M, r, P, to, ldto, refs_out.data_ptr(), moved.data_ptr(), state.data_ptr(),
                                  at.buffer_info()[0], size.buffer_info()[0], step.buffer_info()[0], len(at),
@@ -1102,9 +1112,13 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     k = beams if k is None else k
     x, ld = _matrix(logits, "logits", logits.dtype, (n * beams, vocab), dev)
     sc = _dense(scores, "scores", torch.float32, (n, beams), dev)
-    scores_out = _new_or(scores_out, "scores_out", scores, (n, k), torch.float32, dev)
-    parents = _new_or(parents, "parents", scores, (n, k), torch.int32, dev)
-    tokens = _new_or(tokens, "tokens", scores, (n, k), torch.int32, dev)
+    if scores_out is None and parents is None and tokens is None:    # parts of one allocation
+        scores_out, parents, tokens = scores.new_empty((3, n, k)).unbind(0)
+        parents, tokens = parents.view(torch.int32), tokens.view(torch.int32)
+    else:
+        scores_out = _new_or(scores_out, "scores_out", scores, (n, k), torch.float32, dev)
+        parents = _new_or(parents, "parents", scores, (n, k), torch.int32, dev)
+        tokens = _new_or(tokens, "tokens", scores, (n, k), torch.int32, dev)
     h = ho = None
     T = ldh = ldho = 0
     if history is not None:
@@ -1112,7 +1126,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
         h, ldh = _matrix(history, "history", torch.int32, (n * beams, T), dev)
         if history_out is None:
             history_out = history.new_empty((n * k, T + 1))
-        ho, ldho = _matrix(history_out, "history_out", torch.int32, (n * k, T + 1), dev)
+            ho, ldho = history_out.data_ptr(), T + 1
+        else:
+            ho, ldho = _matrix(history_out, "history_out", torch.int32, (n * k, T + 1), dev)
     workspace = _scratch(beam_select_workspace(n, beams, vocab, k), "beam_select", workspace, logits.device)
     st = _lib.i8mm_beam_select(x, ld, _DTYPES[logits.dtype], n, beams, vocab, sc, k, scores_out.data_ptr(), parents.data_ptr(),
                                tokens.data_ptr(), h, ldh, T, ho, ldho, workspace.data_ptr(), _raw_stream(dev))

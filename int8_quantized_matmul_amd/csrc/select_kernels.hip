@@ -380,14 +380,15 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
         }
         __syncthreads();
         if (a.history_out) {
-            // four tokens a thread and four times that in flight
+            // four tokens a thread and kEach times that in flight
+            constexpr int kEach = 8;
             const int64_t quads = (a.T + 3) / 4, pieces = quads * a.k;
-            for (int64_t p0 = threadIdx.x; p0 < pieces; p0 += 4 * kThreads) {
-                v4i t[4];
-                int32_t* to[4];
-                int n[4];
+            for (int64_t p0 = threadIdx.x; p0 < pieces; p0 += kEach * kThreads) {
+                v4i t[kEach];
+                int32_t* to[kEach];
+                int n[kEach];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kEach; ++q) {
                     const int64_t p = p0 + q * kThreads;
                     n[q] = 0;
                     if (p >= pieces) continue;
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kEach; ++q) {
                     if (n[q] == 4) {
                         __builtin_memcpy(to[q], &t[q], 16);
                     } else {
