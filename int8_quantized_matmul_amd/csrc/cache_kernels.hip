@@ -356,27 +356,47 @@ constexpr int kAlonePages = 32768;
 
 __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, const ForkScratch w) {
     __shared__ int s_refs[kAlonePages];
-    __shared__ int s_sum[kPlanThreads / 64], s_more[kPlanThreads], s_used[kPlanThreads];
+    __shared__ int s_sum[kPlanThreads / 64], s_more[kPlanThreads], s_len[kPlanThreads];
     const int tid = static_cast<int>(threadIdx.x);
+    // All that does not depend on anything first, and the tables' lines into the cache: memory
+    // is waited for once here.
+    int seen = 0;
+    const int lines = (a.max_pages + 31) / 32, all_lines = static_cast<int>(a.n) * lines;
+    if (all_lines <= 4 * kPlanThreads) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int l = tid + q * kPlanThreads, i = l / lines;
+            if (l < all_lines) seen ^= a.tables[i * a.ldt + 32 * (l - i * lines)];
+        }
+    }
+    Asked s = {-1, 0, 0, -1};
+    if (tid < a.n_out) {
+        s.parent = parent_of(a, tid);
+        s.grow = grown_by(a, tid);
+    }
+    if (tid < a.n) s_len[tid] = clamped_len(a, tid);
 #pragma unroll 8
     for (int p = tid; p < a.n_pages; p += kPlanThreads) s_refs[p] = a.refs[p];
+    asm volatile("" ::"v"(seen));                // (not to be left out)
     s_more[tid] = -1;                            // children, less itself
-    if (tid < a.n) s_used[tid] = (clamped_len(a, tid) + a.page - 1) / a.page;
-    const Asked s = asked_by(a, tid);
+    __syncthreads();
+    if (s.parent >= 0) {
+        s.len = s_len[s.parent];
+        s.page = written_page(a, s.parent, s.len, s.grow);
+        atomicAdd(&s_more[s.parent], 1);
+    }
     if (s.page >= 0) {
         w.keeper[s.page] = -1;
         w.growing[s.page] = 0;
     }
     __syncthreads();
-    if (s.parent >= 0) atomicAdd(&s_more[s.parent], 1);
     if (s.page >= 0) {
         atomicMax(&w.keeper[s.page], tid);
         atomicAdd(&w.growing[s.page], 1);
     }
-    __syncthreads();
     // 16 lanes an old sequence
     for (int i = tid / 16; i < a.n; i += kPlanThreads / 16) {
-        const int more = s_more[i], used = s_used[i];
+        const int more = s_more[i], used = (s_len[i] + a.page - 1) / a.page;
         if (more == 0) continue;
 #pragma unroll 8
         for (int c = tid % 16; c < used; c += 16) {
