@@ -16,7 +16,7 @@
 //
 // The 16 columns hold the query heads that share a key-value head. One head
 // alone fills one column of 16: the matrix units are idle nearly all the time
-// even so (24 instructions of 16 cycles for 16 KB of cache), since the cache's
+// even so (16 instructions of 16 cycles for 16 KB of cache), since the cache's
 // bytes are what bounds the kernel. The second product takes the probabilities
 // in the cache's own type, rounded once: each is off by half a step, as the result
 // is by its own rounding. (A second part for what is rounded off would cost 0.3 % of
@@ -609,7 +609,8 @@ int most_rounds(int cols, int blocks, int64_t tiles) {
 }
 
 // Up to this many keys a sequence a block takes whole (group, head)s: one launch, and
-// no workspace.
+// no workspace. 32 heads of one sequence of 500 tokens take 8.8 us so and 11.3 split, 96
+// heads of 64 such sequences 253 and 261.
 constexpr int kWholeKeys = I8MM_ATTENTION_WHOLE_KEYS;
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }

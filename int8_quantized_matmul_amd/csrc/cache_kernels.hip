@@ -28,7 +28,9 @@ constexpr int kAppendEach = 4;           // pieces of 16 bytes that a thread has
 
 // A row's pieces are K's, then V's (`pieces` each), over all rows in one line. A block
 // takes kThreads * kAppendEach neighbours: one division by the row's length for the
-// block, 32-bit ones for its threads.
+// block, 32-bit ones for its threads. Memory is the bound: five prompts with 10250 tokens
+// of 32 heads (336 MB moved) 57 us on one cache, 66 on several in turn (5.1 TB/s); 82
+// with one piece a thread, whose four loads depend on each other.
 __global__ __launch_bounds__(kThreads) void k_append(const AppendArgs a, unsigned pieces, unsigned per_head) {
     const unsigned both = 2 * pieces;
     const int64_t total = a.s * both;
@@ -94,7 +96,8 @@ struct PoolBatch {
 };
 
 // One block's piece of the copy of page `from` to page `to`. Through: past the caches, for
-// what is not read again soon.
+// what is not read again soon (a compaction that moves 370 MB takes 152 us so, 4.9 TB/s
+// read and written, and 169 with ordinary accesses; a fork's few pages 7.5 us and 5.5).
 template <bool Through>
 __device__ __forceinline__ void copy_piece(const PoolBatch& b, int piece, int64_t from, int64_t to) {
     int lo = 0, hi = b.n - 1;
@@ -350,8 +353,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_plan(const ForkArgs a, co
 }
 
 // Up to kAlonePages pages and kPlanThreads sequences: all of it in one launch of one block,
-// which holds the counts in shared memory. 512 pages and 16 sequences 7 us instead of 18
-// in five launches, 17600 pages and 256 sequences 13 instead of 30.
+// which holds the counts in shared memory. With the launch that follows, 512 pages and 16
+// sequences take 11 us instead of 21 in five launches, 17600 and 256 24 instead of 28, 32768
+// and 1024 32 instead of 35, 32768 and 64 long ones 22 instead of 34.
 constexpr int kAlonePages = 32768;
 
 __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, const ForkScratch w) {
@@ -464,7 +468,7 @@ int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------- compact
 
-constexpr int kTilePages = 4096;
+constexpr int kTilePages = 1024;
 
 struct CompactScratch {
     int32_t *counts;                     // pages in use of each tile
@@ -554,8 +558,13 @@ __global__ __launch_bounds__(kThreads) void k_compact_place(const CompactArgs a,
     }
 }
 
-// The same in one block, for up to kPlanThreads words of 64 pages: a bit for each page in
-// use, and the pages in use before each word.
+// The same in one block: a bit for each page in use, and the pages in use before each
+// word of 64 (of which there may be as many as threads). 4096 pages 8.6 us with the
+// launch that follows instead of 13.1 in three launches, 16384 13.3 instead of 13.6 (and
+// a launch less for the host), 32768 20 instead of 13.6.
+constexpr int kPlanPages = 16384;
+static_assert(kPlanPages <= 64 * kPlanThreads, "a thread a word");
+
 __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(const CompactArgs a, const CompactScratch w) {
     __shared__ int s_sum[kPlanThreads / 64], s_before[kPlanThreads];
     __shared__ uint64_t s_mask[kPlanThreads];
@@ -680,7 +689,7 @@ hipError_t launch_cache_compact(const CompactArgs& a, const Pools& pools, void* 
     w.src = take(a.n_pages);
     w.dst = take(a.n_pages);
     w.count = take(1);
-    if (a.n_pages <= 64 * kPlanThreads) {
+    if (a.n_pages <= kPlanPages) {
         k_compact_plan<<<1, kPlanThreads, 0, stream>>>(a, w);
     } else {
         k_compact_count<<<tiles, kThreads, 0, stream>>>(a, w);
