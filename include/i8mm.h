@@ -687,6 +687,8 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
  *     counts in) hold each page. A page is free if its count is 0 or less; a page
  *     that a table holds but refs does not count may be taken, and its contents
  *     are then lost.
+ *   - Calls that overlap may not share a workspace, nor an output, nor may what
+ *     one of them reads be changed while it runs.
  */
 /* Limits: pages of a pool, tokens of a page, pages of a sequence (and max_pages
  * * page < 2^31 - 4096), sequences of a call, features of a head (a multiple of
@@ -701,7 +703,7 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
 #define I8MM_CACHE_MAX_APPEND 16777216
 #define I8MM_BEAM_MAX 64
 #define I8MM_BEAM_MAX_VOCAB 16777216
-#define I8MM_ATTENTION_WHOLE_KEYS 512
+#define I8MM_ATTENTION_WHOLE_KEYS 1024
 
 /*
  * Appends rows to their sequences' pages: for each i < s, with q = seq[i]
@@ -801,9 +803,11 @@ size_t i8mm_decode_attention_workspace_bytes(int64_t n, int64_t heads, int64_t k
  * once for the group. It changes the speed alone; 1 is always right. workspace:
  * i8mm_decode_attention_workspace_bytes(...) bytes, 256-byte aligned, contents
  * unspecified before and after; NULL is accepted if max_pages * page is at most
- * I8MM_ATTENTION_WHOLE_KEYS.
+ * I8MM_ATTENTION_WHOLE_KEYS (half of that if beams is more than 1).
  * What lies behind a sequence's last token never reaches it, NaN and infinity
- * included.
+ * included. Among its tokens they give what the formulas give, except that an
+ * infinite value whose weight is rounded to 0 (below 2^-40 of the largest in
+ * fp16, 2^-126 in bf16) gives NaN.
  */
 i8mm_status i8mm_decode_attention(const void* Q, int64_t ldq, int32_t type, int64_t n, int64_t heads, int64_t kv_heads,
                                   int64_t d, const void* K_pages, int64_t k_stride, const void* V_pages,

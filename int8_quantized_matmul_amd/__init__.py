@@ -91,7 +91,7 @@ LORA_MAX_RANK = _native.header_define("I8MM_LORA_MAX_RANK")
 
 # Most beams of a request, and continuations kept of one (I8MM_BEAM_MAX).
 BEAM_MAX = _native.header_define("I8MM_BEAM_MAX")
-# Up to this many positions a sequence decode_attention takes no workspace.
+# Up to this many positions a sequence (half of that for beams) decode_attention takes no workspace.
 _WHOLE_KEYS = _native.header_define("I8MM_ATTENTION_WHOLE_KEYS")
 
 
@@ -1077,7 +1077,7 @@ def decode_attention(q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tens
     lse = _new_or(lse, "lse", q, (n, heads), torch.float32, dev)
     sl = None if slopes is None else _dense(slopes, "slopes", torch.float32, (heads,), dev)
     ws = None
-    if M * page > _WHOLE_KEYS or workspace is not None:
+    if M * page * (2 if beams > 1 else 1) > _WHOLE_KEYS or workspace is not None:
         workspace = _scratch(decode_attention_workspace(n, heads, kv, d), "decode_attention", workspace, q.device)
         ws = workspace.data_ptr()
     st = _lib.i8mm_decode_attention(x, ldq, _DTYPES[q.dtype], n, heads, kv, d, k, sk, v, sv, P, page, t, ldt, M,

@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
         const int64_t at = u / heads;
         if (at >= before && at < before + mine) {
             int64_t k = g0, from = before, n;
-            while (at >= from + (n = units_of<Beams>(a, w, k))) from += n, ++k;
+            while (k + 1 < w.groups && at >= from + (n = units_of<Beams>(a, w, k))) from += n, ++k;
             s.at_group = k;
             s.at_units = from;
         }
@@ -608,11 +608,6 @@ int most_rounds(int cols, int blocks, int64_t tiles) {
     return r < 1 ? 1 : r < 8 ? static_cast<int>(r) : 8;
 }
 
-// Up to this many keys a sequence a block takes whole (group, head)s: one launch, and
-// no workspace. 32 heads of one sequence of 500 tokens take 8.8 us so and 11.3 split, 96
-// heads of 64 such sequences 253 and 261.
-constexpr int kWholeKeys = I8MM_ATTENTION_WHOLE_KEYS;
-
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <typename T, int NC, int EL, bool Full>
@@ -620,7 +615,7 @@ hipError_t attend_with(const AttendArgs& a, Split w, void* workspace, hipStream_
     w.group = a.heads / a.kv_heads;
     w.parts = (w.group + kCols - 1) / kCols;
     const int heads = a.kv_heads * w.parts;
-    if (static_cast<int64_t>(a.max_pages) * a.page <= kWholeKeys) {
+    if (attention_takes_whole(static_cast<int64_t>(a.max_pages) * a.page, a.beams)) {
         w.groups = a.n;
         w.gb = w.chunks = 1;
         AttendArgs one = a;
@@ -670,6 +665,13 @@ hipError_t attend_type(const AttendArgs& a, void* workspace, hipStream_t stream)
 }
 
 }  // namespace
+
+// Up to so many keys a block takes whole (group, head)s. At 1024: 12 heads of 128
+// sequences 123 us so and 132 split and joined, 32 heads of 16 41 and 47, of one 14 and 11
+// (but a launch less for the host); at 2048 96 heads of 64 993 and 982, and with lengths
+// that differ 532 and 515. Beams that share pages gain by the split path's groups, so
+// they take it earlier.
+bool attention_takes_whole(int64_t keys, int64_t beams) { return keys * (beams > 1 ? 2 : 1) <= I8MM_ATTENTION_WHOLE_KEYS; }
 
 size_t decode_attention_scratch(int64_t n, int, int, int d) {
     return static_cast<size_t>(round256(static_cast<int64_t>(kSumRows) * d * 4) + round256(static_cast<int64_t>(kSumRows) * 2 * 4) +

@@ -147,7 +147,7 @@ i8mm_status i8mm_decode_attention(const void* Q, int64_t ldq, int32_t type, int6
         !valid_pages(n_pages, page, max_pages) || !valid_sequences(n) || !between(beams, 1, I8MM_BEAM_MAX) || n % beams != 0 ||
         !std::isfinite(scale))
         return I8MM_EINVAL;
-    if (!K_pages || !V_pages || (!workspace && max_pages * page > I8MM_ATTENTION_WHOLE_KEYS) || (n != 0 && (!Q || !tables || !lens || !out))) return I8MM_EINVAL;
+    if (!K_pages || !V_pages || (!workspace && !i8mm::attention_takes_whole(max_pages * page, beams)) || (n != 0 && (!Q || !tables || !lens || !out))) return I8MM_EINVAL;
     if (!valid_rows16(Q, ldq, heads * d) || !valid_rows16(out, ldo, heads * d) ||
         !valid_rows16(K_pages, k_stride, kv_heads * page * d) || !valid_rows16(V_pages, v_stride, kv_heads * page * d) ||
         !valid_row(ldt, max_pages) || !aligned4(tables) || !aligned4(lens) || !aligned4(slopes) || !aligned4(lse) ||

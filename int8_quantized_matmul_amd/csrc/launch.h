@@ -275,6 +275,8 @@ struct AttendArgs {
     int64_t ldo;
     float* lse;
 };
+// Whether a block takes all keys of a sequence's head: one launch, no workspace.
+bool attention_takes_whole(int64_t keys, int64_t beams);
 size_t decode_attention_scratch(int64_t n, int heads, int kv_heads, int d);
 hipError_t launch_decode_attention(const AttendArgs& a, void* workspace, hipStream_t stream);
 

@@ -54,7 +54,7 @@ def _attend(q=P, ldq=256, t=F16, n=4, heads=4, kv=2, d=64, Kp=W, ks=2048, Vp=X, 
 
 @pytest.mark.parametrize("kw", [{("ldq" if k == "ldk" else "ldo" if k == "ldv" else k): v for k, v in kw.items()}
                                 for kw in BAD_CACHE]
-                         + [dict(q=None), dict(out=None), dict(lens=None), dict(Kp=None), dict(Vp=None), dict(ws=None, M=33, ldt=33),
+                         + [dict(q=None), dict(out=None), dict(lens=None), dict(Kp=None), dict(Vp=None), dict(ws=None, M=33, ldt=33), dict(ws=None, M=65, ldt=65, beams=1),
                             dict(ws=MIS64), dict(q=MIS8), dict(out=MIS2), dict(out=P), dict(lens=MIS2), dict(slopes=MIS2),
                             dict(lse=MIS2), dict(heads=3), dict(heads=1), dict(heads=65536), dict(heads=0), dict(beams=0),
                             dict(beams=3), dict(beams=65, n=65), dict(scale=float("nan")), dict(scale=float("inf")),
@@ -162,7 +162,7 @@ def test_valid_calls_without_gpu_report_no_device():
         pytest.skip("a GPU is present; covered by the GPU tests")
     assert _append() == _attend() == _fork() == _compact() == _select() == -2
     assert _append(seq=None) == -2 and _append(s=0, K=None, Vr=None, pos=None) == -2 and _append(n=0, tables=None) == -2
-    assert _attend(slopes=None, lse=None) == -2 and _attend(ws=None, M=32, ldt=32) == -2 and _attend(n=0, q=None, out=None, lens=None, tables=None) == -2
+    assert _attend(slopes=None, lse=None) == -2 and _attend(ws=None, M=32, ldt=32) == _attend(ws=None, M=64, ldt=64, beams=1) == -2 and _attend(n=0, q=None, out=None, lens=None, tables=None) == -2
     assert _fork(parents=None, grow=None, at=(), size=(), step=()) == -2 and _fork(n=0, tables=None, lens=None) == -2
     assert _fork(m=0, to=None, lo=None) == -2 and _compact(to=P) == -2 and _compact(n=0, tables=None, to=None) == -2
     assert _select(ho=None, h=None, T=-5) == -2 and _select(h=None, T=0) == -2 and _select(t=F32) == -2

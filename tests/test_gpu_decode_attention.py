@@ -40,6 +40,13 @@ def _check(q, K, V, tables, lens, scale=None, slopes=None, beams=1, **kw):
     return out, lse
 
 
+def _wider(tables, page, keys=1040):
+    """The same tables with room for so many positions: beyond 1024 the work is split and joined."""
+    out = np.full((len(tables), max(tables.shape[1], -(-keys // page))), -1, np.int32)
+    out[:, :tables.shape[1]] = tables
+    return out
+
+
 CASES = [
     # heads, kv_heads, d, page, lengths
     (1, 1, 64, 16, [1]), (1, 1, 8, 16, [5, 0, 33]), (3, 3, 24, 48, [100, 1, 49]), (4, 4, 80, 16, [16, 17, 15, 0, 128, 129]),
@@ -61,6 +68,7 @@ def test_against_the_definition(case, dtype, alibi):
     q = randn(rng, (len(lens), heads * d), dtype, 1.5)
     slopes = torch.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)], device=DEV) if alibi else None
     _check(q, K, V, tables, lens, slopes=slopes)
+    _check(q, K, V, _wider(tables, page), lens, slopes=slopes)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -96,6 +104,7 @@ def test_lengths_and_pages_that_do_not_exist():
     q = randn(rng, (9, heads * d), F16)
     say("  launch: decode_attention, lengths and pages that do not exist")
     _check(q, K, V, tables, lens, slopes=torch.full((heads,), 0.1, device=DEV))
+    _check(q, K, V, _wider(tables, page), lens, slopes=torch.full((heads,), 0.1, device=DEV))
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -112,6 +121,9 @@ def test_large_scores_and_far_biases(dtype):
     _check(q, K, V, tables, lens, scale=-0.01)
     _check(q, K, V, tables, lens, scale=0.0, slopes=torch.tensor([50.0, -50.0, 3.0, 0.0], device=DEV))
     _check(q, K, V, tables, lens, scale=1e-4, slopes=torch.tensor([1e-6, 1.0, -1.0, 1e4], device=DEV))
+    tables = _wider(tables, page)
+    _check(q, K, V, tables, lens)
+    _check(q, K, V, tables, lens, scale=0.0, slopes=torch.tensor([50.0, -50.0, 3.0, 0.0], device=DEV))
 
 
 def test_small_weights_are_not_lost():
@@ -139,7 +151,9 @@ def test_values_near_the_ends_of_the_types():
         say(f"  launch: decode_attention, values of {std}, {dtype}")
         n = lens if std < 1e30 else [3, 2, 5]             # the sum of a few such values is still a number of fp32
         K, V = pool(rng, tables, n, pages, 2, page, d, dtype), pool(rng, tables, n, pages, 2, page, d, dtype, std=std)
-        _check(randn(rng, (3, 2 * d), dtype), K, V, tables, n)
+        q = randn(rng, (3, 2 * d), dtype)
+        _check(q, K, V, tables, n)
+        _check(q, K, V, _wider(tables, page), n)
 
 
 def test_values_that_are_not_finite():
@@ -155,8 +169,13 @@ def test_values_that_are_not_finite():
     V[int(tables[2, 0]), 0, 0, 0] = float("nan")
     K[int(tables[3, 1]), 0, 4, :] = 65504.0
     q[3, :2 * d] = 65504.0
+    for table in (tables, _wider(tables, page)):
+        _not_finite(q, K, V, tables, table, lens, d)
+
+
+def _not_finite(q, K, V, tables, table, lens, d):
     say("  launch: decode_attention, values that are not finite")
-    out, lse = i8.decode_attention(q, K, V, ints(tables), ints(lens))
+    out, lse = i8.decode_attention(q, K, V, ints(table), ints(lens))
     torch.cuda.synchronize()
     o, s = wide(out).reshape(4, 6, d), wide(lse)
     assert np.isnan(o[0, 2:4]).all() and np.isnan(s[0, 2:4]).all()
@@ -217,6 +236,7 @@ def test_beams_that_share_pages(heads, kv, d, page, beams, shared, own):
     K, V = (pool(rng, tables, lens, pages, kv, page, d, F16) for _ in range(2))
     q = randn(rng, (2 * beams, heads * d), F16)
     slopes = torch.tensor([0.5 / (h + 1) for h in range(heads)], device=DEV)
+    tables = _wider(tables, page, 528)                # beyond what beams take whole
     say(f"  launch: decode_attention, {beams} beams, {heads} heads of {kv}, shared {shared}")
     _check(q, K, V, tables, lens, slopes=slopes, beams=beams)
     # pages that only some share, at other places of their rows, and lengths that differ over shared pages
@@ -235,7 +255,7 @@ def test_same_result_every_time_and_on_another_stream():
     lens, page, kv, d = [1000, 3, 517, 64], 16, 4, 128
     tables, pages = paged(rng, lens, page)
     K, V = (pool(rng, tables, lens, pages, kv, page, d, F16) for _ in range(2))
-    q, t, n = randn(rng, (4, 8 * d), F16), ints(tables), ints(lens)
+    q, t, n = randn(rng, (4, 8 * d), F16), ints(_wider(tables, page)), ints(lens)
     say("  launch: decode_attention, repeated")
     first = i8.decode_attention(q, K, V, t, n)
     ws = torch.empty(i8.decode_attention_workspace(4, 8, kv, d), dtype=torch.uint8, device=DEV)
@@ -256,7 +276,7 @@ def test_captured_and_replayed():
     page, kv, d, n = 16, 2, 64, 5
     tables, pages = paged(rng, [200] * n, page)
     K, V = (pool(rng, tables, [200] * n, pages, kv, page, d, BF16) for _ in range(2))
-    q, t, lens = randn(rng, (n, 4 * d), BF16), ints(tables), ints([1] * n)
+    q, t, lens = randn(rng, (n, 4 * d), BF16), ints(_wider(tables, page)), ints([1] * n)
     ws = torch.empty(i8.decode_attention_workspace(n, 4, kv, d), dtype=torch.uint8, device=DEV)
     outs = [(torch.empty_like(q), torch.empty((n, 4), device=DEV)) for _ in range(2)]
     say("  launch: decode_attention, captured")
@@ -287,6 +307,8 @@ def test_many_sequences():
     K, V = (torch.from_numpy(rng.normal(size=(pages, 1, page, d)).astype(np.float32)).to(DEV).half() for _ in range(2))
     q = randn(rng, (n, d), F16)
     say("  launch: decode_attention, 5000 sequences")
+    _check(q, K, V, tables, lens)
+    tables = _wider(tables, page)
     _check(q, K, V, tables, lens)
     _check(q, K, V, tables, lens, beams=10)
 
