@@ -359,7 +359,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_plan(const ForkArgs a, co
 constexpr int kAlonePages = 32768;
 
 __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, const ForkScratch w) {
-    __shared__ int s_refs[kAlonePages];
+    __shared__ __attribute__((aligned(16))) int s_refs[kAlonePages];
     __shared__ int s_sum[kPlanThreads / 64], s_more[kPlanThreads], s_len[kPlanThreads];
     const int tid = static_cast<int>(threadIdx.x);
     // All that does not depend on anything first, and the tables' lines into the cache: memory
@@ -379,8 +379,21 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, c
         s.grow = grown_by(a, tid);
     }
     if (tid < a.n) s_len[tid] = clamped_len(a, tid);
-#pragma unroll 8
-    for (int p = tid; p < a.n_pages; p += kPlanThreads) s_refs[p] = a.refs[p];
+    // counts by fours, all of a thread's in flight at once
+    v4i four[kAlonePages / (4 * kPlanThreads)];
+#pragma unroll
+    for (int q = 0; q < kAlonePages / (4 * kPlanThreads); ++q) {
+        const int p = 4 * (tid + q * kPlanThreads);
+        if (p + 3 < a.n_pages) {
+            __builtin_memcpy(&four[q], a.refs + p, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) four[q][e] = p + e < a.n_pages ? a.refs[p + e] : 0;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kAlonePages / (4 * kPlanThreads); ++q)
+        if (4 * (tid + q * kPlanThreads) < a.n_pages) *reinterpret_cast<v4i*>(s_refs + 4 * (tid + q * kPlanThreads)) = four[q];
     asm volatile("" ::"v"(seen));                // (not to be left out)
     s_more[tid] = -1;                            // children, less itself
     __syncthreads();
@@ -433,8 +446,16 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, c
     }
     if (tid == 0) note_state(a, w, plan);
     __syncthreads();
-#pragma unroll 8
-    for (int p = tid; p < a.n_pages; p += kPlanThreads) a.refs_out[p] = s_refs[p];
+    for (int p = 4 * tid; p < a.n_pages; p += 4 * kPlanThreads) {
+        const v4i refs = *reinterpret_cast<const v4i*>(s_refs + p);
+        if (p + 3 < a.n_pages) {
+            __builtin_memcpy(a.refs_out + p, &refs, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p + e < a.n_pages) a.refs_out[p + e] = refs[e];
+        }
+    }
 }
 
 __device__ __forceinline__ Team whole_grid() {

@@ -319,6 +319,14 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t b = blockIdx.x; b < a.n; b += gridDim.x) {
         const int64_t row0 = b * a.beams;
+        const int each = parts * a.k, all = a.beams * each, lists = a.beams * parts;
+        const float* value = w.value + row0 * each;
+        const int32_t* token = w.token + row0 * each;
+        // a candidate's place: the lists' first ones come first, so that few of the others are put in
+        const auto place = [&](int c) { return c % lists * a.k + c / lists; };
+        const int c1 = wave * kWave + lane;
+        const float value1 = c1 < all ? value[place(c1)] : 0.0f;     // the first of each lane, on their way while the sums are taken
+        const int token1 = c1 < all ? token[place(c1)] : kNone;
         {
             // as many lanes a beam as there are, up to a wavefront
             const int lanes = a.beams <= 4 ? 64 : a.beams <= 8 ? 32 : a.beams <= 16 ? 16 : a.beams <= 32 ? 8 : 4;
@@ -340,23 +348,21 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
         }
         __syncthreads();
         Best<double> best;
-        const int each = parts * a.k, all = a.beams * each;
-        const float* value = w.value + row0 * each;
-        const int32_t* token = w.token + row0 * each;
-        // the parts' first candidates come first, so that few of the others are put in
         for (int c0 = wave * kWave; c0 < all; c0 += kThreads) {
-            const int c = c0 + lane, rank = c / (a.beams * parts), list = c - rank * (a.beams * parts);
-            const int beam = list / parts;
+            const int c = c0 + lane, beam = c % lists / parts;
+            const bool firsts = c0 == wave * kWave;
             const double none = minus_infinity();
             double t = none;
             int v = kNone;
             if (c < all) {
                 const double lse = s_lse[beam];
                 if (lse == lse) {
-                    v = token[list * a.k + rank];
-                    t = a.scores[row0 + beam] + (value[list * a.k + rank] - lse);
-                } else if (list == beam * parts) {
-                    v = rank < a.vocab ? rank : kNone;   // nothing to choose by: the lowest tokens, with no weight
+                    v = firsts ? token1 : token[place(c)];
+                    t = a.scores[row0 + beam] + ((firsts ? value1 : value[place(c)]) - lse);
+                } else if (c % lists == beam * parts) {
+                    // nothing to choose by: the lowest tokens, with no weight
+                    const int rank = c / lists;
+                    v = rank < a.vocab ? rank : kNone;
                 }
             }
             const int at = v == kNone ? kNone : beam * a.vocab + v;
