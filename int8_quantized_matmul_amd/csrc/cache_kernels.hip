@@ -241,20 +241,32 @@ __device__ __forceinline__ void fork_share(const ForkArgs& a, const ForkScratch&
     }
 }
 
-// The sum of v over the threads before this one, and over all of them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int shifted(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false); }
+
+// The sum of v over the lanes up to this one, by lane permutes in the adder's operand path:
+// shifts within 16 lanes, then the last lane of each 16 and 32 to the ones behind.
+__device__ __forceinline__ int scan_lanes(int v) {
+    v += shifted<0x111, 0xf>(v);
+    v += shifted<0x112, 0xf>(v);
+    v += shifted<0x114, 0xf>(v);
+    v += shifted<0x118, 0xf>(v);
+    v += shifted<0x142, 0xa>(v);
+    v += shifted<0x143, 0xc>(v);
+    return v;
+}
+
+// The sum of v over the threads before this one, and over all of them (of up to 16 wavefronts).
 __device__ __forceinline__ int block_scan(int v, int* s_sum, int* total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int upto = wave_inclusive_scan(v, lane);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int upto = scan_lanes(v);
     if (lane == 63) s_sum[wave] = upto;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int k = 0; k < waves; ++k) {
-        if (k < wave) before += s_sum[k];
-        all += s_sum[k];
-    }
+    const int sums = scan_lanes(lane < waves ? s_sum[lane] : 0);
     __syncthreads();
-    *total = all;
-    return before + upto - v;
+    *total = __builtin_amdgcn_readlane(sums, 63);
+    return (wave > 0 ? __builtin_amdgcn_readlane(sums, wave - 1) : 0) + upto - v;
 }
 
 // What new sequence j goes on from, and asks for.
@@ -411,14 +423,21 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, c
         atomicMax(&w.keeper[s.page], tid);
         atomicAdd(&w.growing[s.page], 1);
     }
-    // 16 lanes an old sequence
-    for (int i = tid / 16; i < a.n; i += kPlanThreads / 16) {
+    // eight lanes an old sequence, 16 of a lane's entries in flight at once
+    constexpr int kLanes = 8, kEntries = 16;
+    for (int i = tid / kLanes; i < a.n; i += kPlanThreads / kLanes) {
         const int more = s_more[i], used = (s_len[i] + a.page - 1) / a.page;
         if (more == 0) continue;
-#pragma unroll 8
-        for (int c = tid % 16; c < used; c += 16) {
-            const int id = a.tables[i * a.ldt + c];
-            if (id >= 0 && id < a.n_pages) atomicAdd(&s_refs[id], more);
+        for (int c0 = tid % kLanes; c0 < used; c0 += kLanes * kEntries) {
+            int id[kEntries];
+#pragma unroll
+            for (int q = 0; q < kEntries; ++q) {
+                const int c = c0 + q * kLanes;
+                id[q] = c < used ? a.tables[i * a.ldt + c] : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < kEntries; ++q)
+                if (id[q] >= 0 && id[q] < a.n_pages) atomicAdd(&s_refs[id[q]], more);
         }
     }
     __syncthreads();
