@@ -366,8 +366,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_plan(const ForkArgs a, co
 
 // Up to kAlonePages pages and kPlanThreads sequences: all of it in one launch of one block,
 // which holds the counts in shared memory. With the launch that follows, 512 pages and 16
-// sequences take 11 us instead of 21 in five launches, 17600 and 256 24 instead of 28, 32768
-// and 1024 32 instead of 35, 32768 and 64 long ones 22 instead of 34.
+// sequences take 10 us instead of 19 in five launches, 17600 and 256 17 instead of 25, 32768
+// and 1024 30 instead of 33, 32768 and 64 long ones 19 instead of 32.
 constexpr int kAlonePages = 32768;
 
 __global__ __launch_bounds__(kPlanThreads) void k_fork_alone(const ForkArgs a, const ForkScratch w) {
@@ -599,9 +599,9 @@ __global__ __launch_bounds__(kThreads) void k_compact_place(const CompactArgs a,
 }
 
 // The same in one block: a bit for each page in use, and the pages in use before each
-// word of 64 (of which there may be as many as threads). 4096 pages 8.6 us with the
-// launch that follows instead of 13.1 in three launches, 16384 13.3 instead of 13.6 (and
-// a launch less for the host), 32768 20 instead of 13.6.
+// word of 64 (of which there may be as many as threads). 4096 pages 7.9 us with the
+// launch that follows instead of 11.9 in three launches, 16384 12.3 in either (and a
+// launch less for the host), and each further 16384 some 6 more here, 0.1 there.
 constexpr int kPlanPages = 16384;
 static_assert(kPlanPages <= 64 * kPlanThreads, "a thread a word");
 
