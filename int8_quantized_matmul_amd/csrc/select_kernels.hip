@@ -7,9 +7,10 @@
 // each lane, a running maximum and sum of exponentials, and, one a lane, the
 // part's k best so far in order (within a row the logits alone order the
 // tokens). What is not above the last of them costs a comparison; what is, is
-// put in its place by a shift of the lanes behind it. A second launch joins a
-// request's parts: the sums in fp64, then the k best of the parts' candidates,
-// which are sorted over the lanes and merged where they are many.
+// kept until there is more of it, then sorted over the lanes and merged with
+// them. A second launch joins a request's parts: the sums in fp64, then the k
+// best of the parts' candidates. A few at a time are put in their places one
+// after the other, by a shift of the lanes behind.
 
 #include "../../include/i8mm.h"
 #include "launch.h"
@@ -201,18 +202,26 @@ struct SelectScratch {
     int32_t* token;                              // [rows][parts][k]
 };
 
+constexpr int kHeld = 32;                        // tokens that wait before they are put in order
+static_assert(kHeld <= kWave, "the room in k_select_scan");
+
 // Part of a row, a quarter of it a wavefront: a running maximum and sum of
-// exponentials, and the k largest logits. A wavefront takes `Steps` steps at once: the
-// more tokens are compared with one bar, the fewer are put in only to be pushed out
-// again. 64 x 8 beams over 50272 tokens in fp32, k = 16 (103 MB): 36 us with one
-// step, 34 with two or three, 40 with four (a longer program and a longer tail); 19
-// without the selection, which is what memory takes: each wavefront puts in some 50
-// tokens, one after the other.
+// exponentials, and the k largest logits. Tokens that are not below the bar wait in
+// shared memory until there are kHeld of them, which are sorted over the lanes and
+// merged with the k best; the first bar is the k-th of the lanes' largest of the first
+// steps. A wavefront takes `Steps` steps of 512 tokens at once. 64 x 8 beams over 50272
+// tokens in fp32 (103 MB): k = 16 in 29.5 us with two steps, 30.5 with one, 39 with
+// three (of registers fewer wavefronts are left), 35 if each token is put in its place
+// when it is met; k = 64 in 42 instead of 75 so, rows that rise 87 instead of 131. 19
+// without the selection, which is what memory takes.
 template <typename T, int Steps>
 __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, const SelectScratch w, int parts, int quarter) {
     __shared__ float s_value[kWaves][kWave], s_m[kWaves], s_l[kWaves];
     __shared__ volatile float s_floor[kWaves];   // the k-th best of each wavefront so far: what lies below is not wanted
     __shared__ int s_index[kWaves][kWave];
+    // wanted tokens of each wavefront, not yet put in: fewer than kWave from before, and a step's
+    __shared__ float s_wanted[kWaves][kWave + Steps * kStep];
+    __shared__ int s_token[kWaves][kWave + Steps * kStep];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t items = a.n * a.beams * parts;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -225,6 +234,8 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
         if (lane == 0) s_floor[wave] = -INFINITY;
         __syncthreads();
         Best<float> best;
+        int held = 0;
+        float bar = -INFINITY;                   // what is below it is not wanted
         float m = -INFINITY, l = 0.0f;
         Eight<T> next[Steps];
 #pragma unroll
@@ -254,25 +265,47 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
                 for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((f[q][i] - off) * kLog2e);
             l = __builtin_fmaf(l, m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - off) * kLog2e), s);
             m = up;
-            // What is below the bar is not wanted: nothing below another wavefront's k-th; of what this one
-            // has k of, nothing up to the k-th (a later token loses a tie).
-            const float floor = fmaxf(fmaxf(s_floor[0], s_floor[1]), fmaxf(s_floor[2], s_floor[3]));
-            float bar = best.last_index == kNone ? floor : fmaxf(floor, above(best.last));
+            if (v0 == from) {
+                // at first, nothing below the k-th of the lanes' largest
+                float sorted = most;
+                sort_values(sorted, lane);
+                bar = lane_float(sorted, a.k - 1);
+                if (lane == 0) s_floor[wave] = bar;
+            }
+            bar = fmaxf(bar, fmaxf(fmaxf(s_floor[0], s_floor[1]), fmaxf(s_floor[2], s_floor[3])));
             if (__any(most >= bar)) {
-                if (v0 == from) {
-                    // at first, nothing below the k-th of the lanes' largest
-                    float sorted = most;
-                    sort_values(sorted, lane);
-                    bar = fmaxf(bar, lane_float(sorted, a.k - 1));
-                }
 #pragma unroll
                 for (int q = 0; q < Steps; ++q)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint64_t left = __ballot((f[q][i] >= bar) & (v + q * kStep + i < to));
-                        if (left) best.offer_few(f[q][i], v + q * kStep + i, left, a.k, lane);
+                        const bool wanted = (f[q][i] >= bar) & (v + q * kStep + i < to);
+                        const uint64_t left = __ballot(wanted);
+                        if (left) {
+                            const int at = held + __builtin_amdgcn_mbcnt_hi(left >> 32, __builtin_amdgcn_mbcnt_lo(left, 0));
+                            if (wanted) {
+                                s_wanted[wave][at] = f[q][i];
+                                s_token[wave][at] = v + q * kStep + i;
+                            }
+                            held += __builtin_popcountll(left);
+                        }
                     }
-                if (lane == 0) s_floor[wave] = best.last;
+            }
+            if (held >= kHeld || (v0 + Steps * kStep >= to && held > 0)) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                for (int c = 0; c < held; c += kWave) {
+                    const bool real = c + lane < held;
+                    const float fv = real ? s_wanted[wave][c + lane] : -INFINITY;
+                    const int fi = real ? s_token[wave][c + lane] : kNone;
+                    const uint64_t left = __ballot(real & best.wants(fv, fi));
+                    if (left) best.offer(fv, fi, left, a.k, lane);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                held = 0;
+                // of what this one has k of, nothing up to the k-th (a later token loses a tie)
+                if (best.last_index != kNone) {
+                    bar = fmaxf(bar, above(best.last));
+                    if (lane == 0) s_floor[wave] = best.last;
+                }
             }
         }
         const float top = wave_max_f(m);

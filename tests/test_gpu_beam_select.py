@@ -99,6 +99,25 @@ def test_ascending_and_descending_logits():
         assert not differ.any()
 
 
+@pytest.mark.parametrize("k", [1, 31, 33, 64])
+def test_best_in_one_place(k):
+    """All that is chosen lies together, anywhere in rows of several steps, rising, falling or of few different values."""
+    V, rows = 20011, 512                              # two parts a row
+    rng = np.random.default_rng(k)
+    x = rng.integers(-40, 0, size=(rows, V)).astype(np.float32) / 8
+    for r in range(rows):
+        at = [0, 500, 1000, 2490, 9980, 10010, V - 130, V - k][r % 8]
+        size = min(V - at, 130) if r % 3 else min(V - at, k)
+        x[r, at:at + size] = [np.arange(size) / 16, -np.arange(size) / 16 + 9, np.arange(size) // 40, np.zeros(size)][r // 8 % 4] + 1
+    logits = torch.from_numpy(x).to(DEV)
+    scores = torch.zeros(rows, 1, device=DEV)
+    say(f"  launch: beam_select {rows} x 1 x {V}, k {k}")
+    got = i8.beam_select(logits, scores, k)
+    order = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(got[2].cpu().numpy(), order)
+    _check(logits[:24], scores[:24], k)
+
+
 def test_what_leaves_nothing():
     """Masked tokens (-inf and the type's lowest value), beams that have ended (a score of -inf), rows without a token left,
     NaN and +inf logits, scores that are not finite."""
