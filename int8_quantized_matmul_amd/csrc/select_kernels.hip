@@ -342,12 +342,14 @@ __global__ __launch_bounds__(kThreads) void k_select_scan(const SelectArgs a, co
 
 // A block a request: the sums of its rows, the candidates of all their parts, the chosen
 // ones' histories. One wait after another bounds it: 12 us for 64 requests of 8 beams, k
-// = 16 and histories of 700 tokens, 8 for one request of 4 beams in 25 parts each.
+// = 16 and histories of 700 tokens, 8 for one request of 4 beams in 25 parts each; 19 for
+// one of 7872 candidates, k = 64 (22 if each is loaded when it is looked at).
 __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, const SelectScratch w, int parts) {
     __shared__ double s_value[kWaves][kWave];
     __shared__ int s_index[kWaves][kWave];
     static_assert(I8MM_BEAM_MAX * 4 <= kThreads && I8MM_BEAM_MAX <= kWave, "four lanes a beam, a lane a continuation");
     __shared__ double s_lse[kWave];              // of each beam; NaN: the beam leaves nothing
+    __shared__ double s_score[kWave];
     __shared__ int s_parent[kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t b = blockIdx.x; b < a.n; b += gridDim.x) {
@@ -357,9 +359,13 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
         const int32_t* token = w.token + row0 * each;
         // a candidate's place: the lists' first ones come first, so that few of the others are put in
         const auto place = [&](int c) { return c % lists * a.k + c / lists; };
-        const int c1 = wave * kWave + lane;
-        const float value1 = c1 < all ? value[place(c1)] : 0.0f;     // the first of each lane, on their way while the sums are taken
-        const int token1 = c1 < all ? token[place(c1)] : kNone;
+        float x = 0.0f;                          // a lane's candidate, on its way while the one before is looked at
+        int v = kNone;
+        const auto fetch = [&](int c) {
+            x = c < all ? value[place(c)] : 0.0f;
+            v = c < all ? token[place(c)] : kNone;
+        };
+        fetch(wave * kWave + lane);
         {
             // as many lanes a beam as there are, up to a wavefront
             const int lanes = a.beams <= 4 ? 64 : a.beams <= 8 ? 32 : a.beams <= 16 ? 16 : a.beams <= 32 ? 8 : 4;
@@ -377,29 +383,28 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
             if (there && p0 == 0) {
                 const double lse = top + log(l), score = a.scores[row0 + i];
                 s_lse[i] = (lse - lse) + (score - score) == 0.0 ? lse : NAN;
+                s_score[i] = score;
             }
         }
         __syncthreads();
         Best<double> best;
         for (int c0 = wave * kWave; c0 < all; c0 += kThreads) {
             const int c = c0 + lane, beam = c % lists / parts;
-            const bool firsts = c0 == wave * kWave;
             const double none = minus_infinity();
             double t = none;
-            int v = kNone;
+            int at = kNone;
             if (c < all) {
                 const double lse = s_lse[beam];
                 if (lse == lse) {
-                    v = firsts ? token1 : token[place(c)];
-                    t = a.scores[row0 + beam] + ((firsts ? value1 : value[place(c)]) - lse);
-                } else if (c % lists == beam * parts) {
+                    t = s_score[beam] + (x - lse);
+                    at = v == kNone ? kNone : beam * a.vocab + v;
+                } else if (c % lists == beam * parts && c / lists < a.vocab) {
                     // nothing to choose by: the lowest tokens, with no weight
-                    const int rank = c / lists;
-                    v = rank < a.vocab ? rank : kNone;
+                    at = beam * a.vocab + c / lists;
                 }
             }
-            const int at = v == kNone ? kNone : beam * a.vocab + v;
-            const uint64_t left = __ballot((v != kNone) & best.wants(t, at));
+            if (c0 + kThreads < all) fetch(c + kThreads);
+            const uint64_t left = __ballot((at != kNone) & best.wants(t, at));
             if (left) best.offer(t, at, left, a.k, lane);
         }
         s_value[wave][lane] = best.value;
@@ -410,7 +415,8 @@ __global__ __launch_bounds__(kThreads) void k_select_join(const SelectArgs a, co
                 best.merge_reversed(s_value[o][kWave - 1 - lane], s_index[o][kWave - 1 - lane], a.k, lane);
             if (lane < a.k) {
                 // (in range whatever the workspace holds, should calls that overlap share one)
-                const int rank = best.index / a.vocab, beam = rank < a.beams ? rank : a.beams - 1;
+                const unsigned rank = static_cast<unsigned>(best.index) / static_cast<unsigned>(a.vocab);
+                const int beam = rank < static_cast<unsigned>(a.beams) ? static_cast<int>(rank) : a.beams - 1;
                 const int v = best.index - beam * a.vocab;
                 a.scores_out[b * a.k + lane] = static_cast<float>(best.value);
                 a.parents[b * a.k + lane] = static_cast<int>(row0 + beam);
