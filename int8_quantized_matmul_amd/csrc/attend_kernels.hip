@@ -536,12 +536,17 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
 // The partial sums of one (group, head): the first run's second ones, and the others'
 // first ones, kJoinCols columns a block. Every 16 bytes of the result are summed by one
 // thread, or, where there are fewer of them than threads, by several that take the runs
-// in turn.
+// in turn, kJoinAhead of each on their way at once; the runs' weights lie in shared
+// memory. One sequence of 12274 tokens, 64 heads on 4: 14.5 us, and 26 with a load after
+// the other and the weights taken where they are used; 64 x 96 heads of two parts at most
+// 9 instead of 8. 16 on their way take 13 in each.
 constexpr int kJoinCols = 4;
+constexpr int kJoinAhead = 8;
+constexpr int kJoinRuns = 512;
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, const Split w) {
-    __shared__ float s_m[kJoinCols], s_l[kJoinCols];
+    __shared__ float s_m[kJoinCols], s_l[kJoinCols], s_f[kJoinCols][kJoinRuns];
     __shared__ v4f s_o[kThreads];
     const Split::Join j = w.joins[blockIdx.x];
     if (j.first < 0) return;
@@ -549,16 +554,23 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
     const int kv = j.head / w.parts, part = j.head - kv * w.parts;
     const int cols = w.parts > 1 ? (w.group - part * kCols < kCols ? w.group - part * kCols : kCols) : grp.n * w.group;
     const int n = static_cast<int>(blockIdx.x) - j.first + 1;
-    const auto slot = [&](int b) { return (static_cast<int64_t>(j.first + b) * 2 + (b == 0)) * w.cols; };
-    const int lane = threadIdx.x & 63;
     const int col0 = static_cast<int>(blockIdx.y) * kJoinCols, mine = cols - col0 < kJoinCols ? cols - col0 : kJoinCols;
+    if (mine <= 0) return;
+    const auto row = [&](int b, int c) { return (static_cast<int64_t>(j.first + b) * 2 + (b == 0)) * w.cols + col0 + c; };
+    // of a run without a maximum: nothing if it has seen nothing, all (a NaN) otherwise
+    const auto weight = [&](float m, float l, float most) {
+        return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(m - most);
+    };
+    const int lane = threadIdx.x & 63;
     for (int c = threadIdx.x >> 6; c < mine; c += kWaves) {
         float m = -INFINITY, l = 0.0f;
-        for (int b = lane; b < n; b += kWave) m = fmaxf(m, w.ml[(slot(b) + col0 + c) * 2]);
+        for (int b = lane; b < n; b += kWave) m = fmaxf(m, w.ml[row(b, c) * 2]);
         m = wave_max(m);
         for (int b = lane; b < n; b += kWave) {
-            const float* p = w.ml + (slot(b) + col0 + c) * 2;
-            l += p[0] == -INFINITY ? p[1] : p[1] * __builtin_amdgcn_exp2f(p[0] - m);
+            const float* p = w.ml + row(b, c) * 2;
+            const float f = weight(p[0], p[1], m);
+            l += p[1] * f;
+            if (b < kJoinRuns) s_f[c][b] = f;
         }
         l = wave_sum(l);
         if (lane == 0) {
@@ -566,34 +578,46 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
             s_l[c] = l;
         }
     }
-    if (mine <= 0) return;
     __syncthreads();
-    const int quads = a.d / 4, all = mine * quads, sharers = all < kThreads ? kThreads / all : 1;
-    for (int k0 = 0; k0 < all; k0 += kThreads) {
-        const int by = static_cast<int>(threadIdx.x) / all, k = sharers > 1 ? static_cast<int>(threadIdx.x) - by * all : k0 + static_cast<int>(threadIdx.x);
-        const bool there = sharers > 1 ? by < sharers : k < all;
-        const int c = k / quads, i = 4 * (k - c * quads);
-        v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (there) {
-#pragma unroll 4
-            for (int b = sharers > 1 ? by : 0; b < n; b += sharers) {
-                const int64_t at = slot(b) + col0 + c;
-                const float m = w.ml[at * 2], f = m == -INFINITY ? (w.ml[at * 2 + 1] == 0.0f ? 0.0f : 1.0f)
-                                                                   : __builtin_amdgcn_exp2f(m - s_m[c]);
-                o += *reinterpret_cast<const v4f*>(w.o + at * a.d + i) * f;
-            }
-        }
-        if (sharers > 1) {
-            s_o[threadIdx.x] = o;
+    static_assert(kJoinCols * I8MM_CACHE_MAX_HEAD / 4 <= kThreads, "a thread for each 16 bytes of the result");
+    const int quads = a.d / 4, all = mine * quads, sharers = kThreads / all;
+    const int by = static_cast<int>(threadIdx.x) / all, k = static_cast<int>(threadIdx.x) - by * all;
+    const int c = k / quads, i = 4 * (k - c * quads);
+    v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b0 = 0; b0 < n; b0 += kJoinRuns) {
+        const int count = n - b0 < kJoinRuns ? n - b0 : kJoinRuns;
+        if (b0 > 0) {
             __syncthreads();
-            if (by == 0)
-                for (int b = 1; b < sharers; ++b) o += s_o[b * all + k];
+            for (int x = threadIdx.x; x < mine * kJoinRuns; x += kThreads) {
+                const int xc = x / kJoinRuns, b = x - xc * kJoinRuns;
+                if (b >= count) continue;
+                const float* p = w.ml + row(b0 + b, xc) * 2;
+                s_f[xc][b] = weight(p[0], p[1], s_m[xc]);
+            }
+            __syncthreads();
         }
-        if (there && (sharers == 1 || by == 0)) {
-            const Column col = column_of(w, grp, kv, part, col0 + c);
+        for (int b1 = by; by < sharers && b1 < count; b1 += kJoinAhead * sharers) {
+            v4f part_o[kJoinAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) put<T>(a, col, i + e, o[e], s_m[c], s_l[c]);
+            for (int q = 0; q < kJoinAhead; ++q) {
+                const int b = b1 + q * sharers;
+                if (b < count) part_o[q] = *reinterpret_cast<const v4f*>(w.o + row(b0 + b, c) * a.d + i);
+            }
+#pragma unroll
+            for (int q = 0; q < kJoinAhead; ++q)
+                if (b1 + q * sharers < count) o += part_o[q] * s_f[c][b1 + q * sharers];
         }
+    }
+    if (sharers > 1) {
+        s_o[threadIdx.x] = o;
+        __syncthreads();
+        if (by == 0)
+            for (int b = 1; b < sharers; ++b) o += s_o[b * all + k];
+    }
+    if (by == 0) {
+        const Column col = column_of(w, grp, kv, part, col0 + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put<T>(a, col, i + e, o[e], s_m[c], s_l[c]);
     }
 }
 

@@ -313,6 +313,19 @@ def test_many_sequences():
     _check(q, K, V, tables, lens, beams=10)
 
 
+@pytest.mark.parametrize("heads,kv,d,keys", [(3, 1, 64, 133000), (1, 1, 40, 131072), (6, 1, 128, 70000)])
+def test_one_long_sequence(heads, kv, d, keys):
+    """A result that is joined of more parts than any other test's: up to 1024 of them."""
+    rng = np.random.default_rng(heads)
+    lens = [keys, 5]
+    tables, pages = paged(rng, lens, 64)
+    K, V = (pool(rng, tables, lens, pages, kv, 64, d, F16) for _ in range(2))
+    q = randn(rng, (2, heads * d), F16, 1.5)
+    say(f"  launch: decode_attention, {keys} tokens, {heads} heads of {d}")
+    _check(q, K, V, tables, lens)
+    _check(q, K, V, tables, lens, slopes=torch.full((heads,), 2.0 ** -12, device=DEV))
+
+
 def test_no_sequences_and_refusals():
     K = torch.zeros((4, 2, 16, 64), dtype=F16, device=DEV)
     q = torch.zeros((2, 256), dtype=F16, device=DEV)
