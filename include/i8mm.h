@@ -737,13 +737,15 @@ size_t i8mm_cache_fork_workspace_bytes(int64_t n, int64_t n_out, int64_t n_pages
  * NULL: none) gets room for that many tokens more:
  *   - its last page, if that is not full, is written next. If others hold that
  *     page too, it takes a copy: a fresh page with the same contents in every
- *     pool. Of the sequences that grow in one page the last keeps it if the
- *     others leave it no other holder.
+ *     pool. Of the sequences that grow in one page the last keeps it if it is
+ *     held by nobody but them, since the others take copies.
  *   - then fresh pages follow, up to ceil((len + grow) / page).
  * Fresh pages are the free ones (by refs_out, before any are taken) from the
- * lowest up. A sequence that would exceed max_pages pages does not grow, nor
- * does one whose fresh pages, with those of the ones before it, are more than
- * there are.
+ * lowest up. A sequence that would exceed max_pages pages does not grow (it
+ * holds its last page as one that was not asked to grow), nor does one whose
+ * fresh pages, with those of the ones before it, are more than there are, nor
+ * one that would keep a page which another, short of a page for its copy, still
+ * holds. What does not grow keeps its parent's length and pages.
  *
  * tables_out: [n_out, max_pages] int32 (written; entries not in use are -1);
  * lens_out: [n_out]; refs_out: [n_pages]; state: [4] int32: the pages still

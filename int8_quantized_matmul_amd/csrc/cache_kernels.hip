@@ -7,6 +7,7 @@
 // threads run. What takes time is memory: rows and whole pages are copied in
 // 16-byte pieces.
 
+#include "../../include/i8mm.h"
 #include "launch.h"
 
 #include "device_common.h"
@@ -185,9 +186,10 @@ __device__ __forceinline__ int grown_by(const ForkArgs& a, int64_t j) {
     return g > 0 ? g : 0;
 }
 
-// The page that new sequence j writes on in, or -1: its last one, if that is not full.
+// The page that new sequence j writes on in, or -1: its last one, if that is not full (and
+// the table has room for what it asks for).
 __device__ __forceinline__ int written_page(const ForkArgs& a, int64_t parent, int len, int grow) {
-    if (parent < 0 || grow == 0 || len % a.page == 0) return -1;
+    if (parent < 0 || grow == 0 || len % a.page == 0 || grow > a.max_pages * a.page - len) return -1;
     const int id = a.tables[parent * a.ldt + len / a.page];
     return id >= 0 && id < a.n_pages ? id : -1;
 }
@@ -292,10 +294,18 @@ struct Plan {
     int taken, copies, missed;
 };
 
+// In a page's count of those that write on in it: one of them finds no page for its copy.
+constexpr int kUncopied = 1 << 30;
+static_assert(I8MM_CACHE_MAX_SEQS < kUncopied, "a bit above the count");
+
 // What kPlanThreads sequences get, j this thread's. `held`: the count of the page it writes on in.
+// The last one that writes on in a page keeps it, if the others that hold it all take copies;
+// one that finds no page for its copy still holds it, and then the last one does not grow
+// either. (It comes behind them, and a copy of its own would be short of a page as theirs are.)
 __device__ __forceinline__ void plan_sequences(const ForkArgs& a, const ForkScratch& w, Plan& plan, int64_t j, const Asked& s,
                                                int held, int* s_sum) {
-    int copy = s.page >= 0 && !(fresh_load(&w.keeper[s.page]) == j && fresh_load(&w.growing[s.page]) >= held);
+    const bool keep = s.page >= 0 && fresh_load(&w.keeper[s.page]) == j && (fresh_load(&w.growing[s.page]) & ~kUncopied) >= held;
+    int copy = s.page >= 0 && !keep;
     int ok = s.grow <= a.max_pages * a.page - s.len;
     const int want = ok ? (s.len + s.grow + a.page - 1) / a.page - (s.len + a.page - 1) / a.page + copy : 0;
     // sums stay below 2^31: 1024 sequences of at most 2^20 pages each are taken at a time
@@ -303,6 +313,11 @@ __device__ __forceinline__ void plan_sequences(const ForkArgs& a, const ForkScra
     const int64_t before = plan.wanted + block_scan(want, s_sum, &all);
     plan.wanted += all;
     if (want > 0 && before + want > plan.free_pages) ok = 0;
+    if (plan.wanted > plan.free_pages) {             // (the same for all threads)
+        if (copy && !ok) atomicOr(&w.growing[s.page], kUncopied);
+        __syncthreads();
+        if (keep && (fresh_load(&w.growing[s.page]) & kUncopied)) ok = 0;
+    }
     copy = ok ? copy : 0;
     // copies and sequences that do not grow are at most 1024 each: one scan for both
     int both;

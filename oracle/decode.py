@@ -75,18 +75,22 @@ def fork(tables, lens, refs, page, parents=None, grow=None, pools: Sequence[np.n
                     refs[p] += change
     grow = [0] * len(new) if grow is None else [max(0, int(g)) for g in grow]
     free = [p for p in range(P) if refs[p] <= 0]
-    written = [row[-1] if g and t % page and 0 <= row[-1] < P else None for row, t, g in zip(new, size, grow)]
-    after, wanted, taken, copied, missed = list(refs), 0, 0, [], 0
+    written = [row[-1] if g and t + g <= M * page and t % page and 0 <= row[-1] < P else None
+               for row, t, g in zip(new, size, grow)]
+    after, wanted, taken, copied, missed, uncopied = list(refs), 0, 0, [], 0, set()
     for j, (row, t, g) in enumerate(zip(new, size, grow)):
         w = written[j]
-        copy = w is not None and not (w not in written[j + 1:] and written.count(w) >= refs[w])
+        keep = w is not None and w not in written[j + 1:] and written.count(w) >= refs[w]
+        copy = w is not None and not keep
         if t + g > M * page:
             missed += 1
             continue
         need = -(-(t + g) // page) - len(row) + copy
         wanted += need
-        if need and wanted > len(free):
+        if (need and wanted > len(free)) or (keep and w in uncopied):
             missed += 1
+            if copy:
+                uncopied.add(w)
             continue
         got = free[taken:taken + need]
         taken += need
