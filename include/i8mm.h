@@ -745,7 +745,9 @@ size_t i8mm_cache_fork_workspace_bytes(int64_t n, int64_t n_out, int64_t n_pages
  * holds its last page as one that was not asked to grow), nor does one whose
  * fresh pages, with those of the ones before it, are more than there are, nor
  * one that would keep a page which another, short of a page for its copy, still
- * holds. What does not grow keeps its parent's length and pages.
+ * holds. What does not grow keeps its parent's length and pages, of which others
+ * may hold the last: nothing may be appended to it (a position of -1 leaves its
+ * row out); lens_out[j] above the parent's length tells who grew.
  *
  * tables_out: [n_out, max_pages] int32 (written; entries not in use are -1);
  * lens_out: [n_out]; refs_out: [n_pages]; state: [4] int32: the pages still

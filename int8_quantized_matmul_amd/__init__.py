@@ -970,7 +970,8 @@ def cache_fork(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     `pools` ([n_pages, ...], any type, each page a multiple of 16 bytes).
     Returns (tables, lens, refs, state): state int32 [4] holds the pages still
     free, the pages short, the sequences that could not grow (they keep their
-    length) and the pages copied. The outputs may not be the inputs. A
+    length, and nothing may be appended to them: position -1) and the pages
+    copied. The outputs may not be the inputs. A
     workspace, if given, is a uint8 tensor of cache_fork_workspace(n, n_out,
     n_pages) bytes or more."""
     dev = _gpu_of(tables, "tables", (torch.int32,))
