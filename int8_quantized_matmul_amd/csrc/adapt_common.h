@@ -55,6 +55,14 @@ struct Eight {
     __device__ __forceinline__ void set(int k, float f) { v[k] = from_float<T>(f); }
 };
 
+// -inf in fp64 from a register that the compiler does not look into: as a
+// constant of a whole wavefront it would become a scalar move of a 64-bit
+// literal, which this target has no encoding for and the compiler drops to 0.
+__device__ __forceinline__ double minus_infinity() {
+    float f = -INFINITY;
+    asm("" : "+v"(f));
+    return f;
+}
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(

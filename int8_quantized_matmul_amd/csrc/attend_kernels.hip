@@ -53,8 +53,7 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 
 // kShift: the running maximum's probability is 2^kShift, and the sum has the same
 // factor. In fp16 15: probabilities keep all digits down to 2^-29 of the largest, and
-// sums of 2^31 values times 2^15 stay far below fp32's end. bf16 needs none, and with
-// values near fp32's end there is no room for one.
+// sums of 2^31 values times 2^15 stay far below fp32's end. bf16 needs none.
 template <typename T>
 struct Vec8;
 template <>
@@ -236,6 +235,8 @@ struct Split {
         int64_t group;
         int head;            // key-value head and part
         int first;           // the run with the first partial sums, -1: nothing to join
+        int64_t whole;       // the first (group, head) whose result the run writes itself
+        int64_t beyond;      // and the last one that is not finite, -1: none
     }* joins;                // [runs]
 };
 
@@ -307,13 +308,137 @@ __global__ __launch_bounds__(kThreads) void k_attend_shared(const AttendArgs a, 
     }
 }
 
+// ---------------------------------------------------------------- beyond fp32
+//
+// A sum of values near fp32's end, or a weighted mean that its weights' rounding takes past
+// the type's largest number, is infinite, while the result is not. A column whose result is
+// not finite is computed again by a block in fp64, which has room for all that finite inputs
+// can give, from the definition: the keys' scores for the maximum, then once more for the
+// weights, a key a thread, and the values with 8 features a thread, of 256 / (d / 8) threads
+// that take the keys in turn. It is meant to be rare: one column of 2048 keys of 128 features
+// takes 90 us, of 100000 5.3 ms, all of 64 x 32 with 2048 1.1 ms on top of 0.4. (Smaller
+// weights instead would lose the smallest values, so they would have to follow the values.)
+
+constexpr int kAgainAhead = 4;                   // loads of a thread on their way
+
+struct Again {
+    double value[kThreads];
+    double part[kWaves];
+    int64_t at[kThreads];    // a key's values, -1: there is no key
+};
+
+__device__ __forceinline__ bool finite(float v) { return v - v == 0.0f; }
+
+// f(a, b) over all threads' values, in every thread.
+template <typename F>
+__device__ __forceinline__ double over_block(Again& s, double v, F&& f) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v = f(v, __shfl_xor(v, off, kWave));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s.part[0];
+    for (int k = 1; k < kWaves; ++k) v = f(v, s.part[k]);
+    return v;
+}
+
+// Query head `head` of sequence `seq` over all its keys, out and lse (the block's earlier ones are written over).
+template <typename T>
+__device__ __forceinline__ void attend_again(const AttendArgs& a, Again& s, int64_t seq, int head) {
+    typedef typename Vec8<T>::type vec;
+    const int tid = static_cast<int>(threadIdx.x), len = clamped_len(a, seq), kv = head / (a.heads / a.kv_heads);
+    const T* q = static_cast<const T*>(a.Q) + seq * a.ldq + static_cast<int64_t>(head) * a.d;
+    const auto wide = [](T v) { return static_cast<double>(static_cast<float>(v)); };
+    const int eights = a.d / 8, sharers = kThreads / eights, by = tid / eights, i = 8 * (tid - by * eights);
+    double most = minus_infinity(), l = 0.0, o[8] = {};
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int t0 = 0; t0 < len; t0 += kThreads) {
+            const int t = t0 + tid, id = t < len ? a.tables[seq * a.ldt + t / a.page] : -1;
+            const bool there = id >= 0 && id < a.n_pages;
+            const int64_t page = there ? id : 0, within = (static_cast<int64_t>(kv) * a.page + t % a.page) * a.d;
+            double x = minus_infinity();
+            if (there) {
+                const T* k = static_cast<const T*>(a.K) + page * a.k_stride + within;
+                x = 0.0;
+#pragma unroll 1
+                for (int f0 = 0; f0 < a.d; f0 += 8 * kAgainAhead) {
+                    vec u[kAgainAhead], v[kAgainAhead];
+#pragma unroll
+                    for (int b = 0; b < kAgainAhead; ++b) {
+                        const int f = f0 + 8 * b < a.d ? f0 + 8 * b : 0;
+                        u[b] = *reinterpret_cast<const vec*>(q + f);
+                        v[b] = *reinterpret_cast<const vec*>(k + f);
+                    }
+#pragma unroll
+                    for (int b = 0; b < kAgainAhead; ++b) {
+                        if (f0 + 8 * b >= a.d) break;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x = __builtin_fma(wide(u[b][e]), wide(v[b][e]), x);
+                    }
+                }
+                x *= static_cast<double>(a.scale);
+                if (a.slopes) x = __builtin_fma(static_cast<double>(a.slopes[head]), static_cast<double>(t - (len - 1)), x);
+            }
+            if (pass == 0) {
+                most = fmax(most, x);
+                continue;
+            }
+            const double w = there ? exp(x - most) : 0.0;
+            l += w;
+            __syncthreads();
+            s.value[tid] = w;
+            s.at[tid] = there ? page * a.v_stride + within : -1;
+            __syncthreads();
+            const int count = by >= sharers ? 0 : len - t0 < kThreads ? len - t0 : kThreads;
+#pragma unroll 1
+            for (int k0 = by; k0 < count; k0 += kAgainAhead * sharers) {
+                int64_t at[kAgainAhead];
+                vec v[kAgainAhead];
+#pragma unroll
+                for (int b = 0; b < kAgainAhead; ++b) at[b] = k0 + b * sharers < count ? s.at[k0 + b * sharers] : -1;
+#pragma unroll
+                for (int b = 0; b < kAgainAhead; ++b)
+                    v[b] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.V) + (at[b] < 0 ? 0 : at[b]) + i);
+#pragma unroll
+                for (int b = 0; b < kAgainAhead; ++b) {
+                    if (at[b] < 0) continue;
+                    const double by_w = s.value[k0 + b * sharers];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = __builtin_fma(by_w, wide(v[b][e]), o[e]);
+                }
+            }
+        }
+        if (pass == 0) most = over_block(s, most, [](double x, double y) { return fmax(x, y); });
+    }
+    l = over_block(s, l, [](double x, double y) { return x + y; });
+    T* out = static_cast<T*>(a.out) + seq * a.ldo + static_cast<int64_t>(head) * a.d + i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        s.value[tid] = o[e];
+        __syncthreads();
+        if (by == 0) {
+            double sum = 0.0;
+            for (int k = 0; k < sharers; ++k) sum += s.value[k * eights + tid];
+            out[e] = static_cast<T>(static_cast<float>(sum / l));
+        }
+        __syncthreads();
+    }
+    if (tid == 0 && a.lse) a.lse[seq * a.heads + head] = static_cast<float>(most + log(l));
+}
+
 template <int NC, int EL>
 struct Attend {
     static constexpr int kWide = 16 * EL;
-    float o[kWaves][kCols][kWide];
+    union {
+        float o[kWaves][kCols][kWide];
+        Again again;
+    };
     float m[kWaves][kCols], l[kWaves][kCols];
     int64_t scan[kWaves];
     int64_t at_group, at_units;
+    unsigned beyond;         // the columns whose sums are not finite
 };
 
 // Joins the wavefronts' sums; f(column, feature, o, m, l) for each, o and l relative to the maximum m.
@@ -365,10 +490,18 @@ __device__ __forceinline__ Column column_of(const Split& w, const Group& g, int 
     return {g.first + b, kv * w.group + c - b * w.group};
 }
 
+__device__ __forceinline__ int columns_of(const Split& w, const Group& g, int part) {
+    if (w.parts > 1) return w.group - part * kCols < kCols ? w.group - part * kCols : kCols;
+    return g.n * w.group;
+}
+
+// Feature i of a column's result; whether it is finite.
 template <typename T>
-__device__ __forceinline__ void put(const AttendArgs& a, const Column& c, int i, float o, float m, float l) {
-    static_cast<T*>(a.out)[c.seq * a.ldo + static_cast<int64_t>(c.head) * a.d + i] = static_cast<T>(l == 0.0f ? 0.0f : o / l);
+__device__ __forceinline__ bool put(const AttendArgs& a, const Column& c, int i, float o, float m, float l) {
+    const T v = static_cast<T>(l == 0.0f ? 0.0f : o / l);
+    static_cast<T*>(a.out)[c.seq * a.ldo + static_cast<int64_t>(c.head) * a.d + i] = v;
     if (i == 0 && a.lse) a.lse[c.seq * a.heads + c.head] = log_sum<T>(m, l);
+    return finite(static_cast<float>(v));
 }
 
 // Runs of the split kernel in multiples of the blocks that are resident at once; heads
@@ -408,9 +541,13 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
         const int64_t rounds = total / (static_cast<int64_t>(kBlocks<EL>) * kRunTiles);
         runs = kBlocks<EL> * (rounds < 1 ? 1 : rounds < w.rounds ? rounds : w.rounds);
         runs = total < runs ? total : runs;
-        if (threadIdx.x == 0) w.joins[run].first = -1;
+        if (threadIdx.x == 0) {
+            w.joins[run].first = -1;
+            w.joins[run].beyond = -1;
+        }
         if (run >= runs) return;
     }
+    if (Whole && threadIdx.x == 0) s.beyond = 0;
     int64_t gi, u, end;                             // group; unit of the whole row, and where the run ends
     int64_t units, head, v;                         // the group's units for a head, the head, unit within it
     if (Whole) {
@@ -436,11 +573,12 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
         const int64_t rest = u - s.at_units * heads;
         head = rest / units;
         v = rest - head * units;
+        if (threadIdx.x == 0) w.joins[run].whole = gi * heads + head + (v > 0);
     }
     while (u < end) {
         const Group grp = Beams ? group_at(a, w, gi) : Group{gi, 1};
         const int kv = static_cast<int>(head / w.parts), part = static_cast<int>(head - static_cast<int64_t>(kv) * w.parts);
-        const int cols = w.parts > 1 ? (w.group - part * kCols < kCols ? w.group - part * kCols : kCols) : grp.n * w.group;
+        const int cols = columns_of(w, grp, part);
         const int64_t head_at = static_cast<int64_t>(kv) * a.page * a.d;
         const Column col = column_of(w, grp, kv, part, x);
 
@@ -507,8 +645,18 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
 
         if (Whole || v1 - v == units) {
             join_waves<NC, EL>(s, sum, cols, a.d, wave, lane, [&](int c, int i, float o, float m, float l) {
-                put<T>(a, column_of(w, grp, kv, part, c), i, o, m, l);
+                if (!put<T>(a, column_of(w, grp, kv, part, c), i, o, m, l)) {
+                    if (Whole) atomicOr(&s.beyond, 1u << c);
+                    else w.joins[run].beyond = gi * heads + head;
+                }
             });
+            if (Whole) {
+                for (unsigned beyond = s.beyond; beyond; beyond &= beyond - 1) {
+                    const Column c = column_of(w, grp, kv, part, __builtin_ctz(beyond));
+                    attend_again<T>(a, s.again, c.seq, c.head);
+                }
+                return;
+            }
         } else {
             const int64_t slot = (run * 2 + (v == 0)) * w.cols;
             join_waves<NC, EL>(s, sum, cols, a.d, wave, lane, [&](int c, int i, float o, float m, float l) {
@@ -520,7 +668,9 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
             });
             if (v > 0 && v1 == units && threadIdx.x == 0) {
                 // the run with the first unit, u - v: the last one that starts at or before it
-                w.joins[run] = {gi, static_cast<int>(head), static_cast<int>(((u - v + 1) * runs - 1) / total)};
+                w.joins[run].group = gi;
+                w.joins[run].head = static_cast<int>(head);
+                w.joins[run].first = static_cast<int>(((u - v + 1) * runs - 1) / total);
             }
         }
         u += v1 - v;
@@ -545,14 +695,11 @@ constexpr int kJoinAhead = 8;
 constexpr int kJoinRuns = 512;
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, const Split w) {
+__device__ __forceinline__ void join_runs(const AttendArgs& a, const Split& w, const Split::Join& j, unsigned* beyond) {
     __shared__ float s_m[kJoinCols], s_l[kJoinCols], s_f[kJoinCols][kJoinRuns];
     __shared__ v4f s_o[kThreads];
-    const Split::Join j = w.joins[blockIdx.x];
-    if (j.first < 0) return;
     const Group grp = group_at(a, w, j.group);
-    const int kv = j.head / w.parts, part = j.head - kv * w.parts;
-    const int cols = w.parts > 1 ? (w.group - part * kCols < kCols ? w.group - part * kCols : kCols) : grp.n * w.group;
+    const int kv = j.head / w.parts, part = j.head - kv * w.parts, cols = columns_of(w, grp, part);
     const int n = static_cast<int>(blockIdx.x) - j.first + 1;
     const int col0 = static_cast<int>(blockIdx.y) * kJoinCols, mine = cols - col0 < kJoinCols ? cols - col0 : kJoinCols;
     if (mine <= 0) return;
@@ -617,7 +764,48 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, co
     if (by == 0) {
         const Column col = column_of(w, grp, kv, part, col0 + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) put<T>(a, col, i + e, o[e], s_m[c], s_l[c]);
+        for (int e = 0; e < 4; ++e)
+            if (!put<T>(a, col, i + e, o[e], s_m[c], s_l[c])) atomicOr(beyond, 1u << (col0 + c));
+    }
+}
+
+// And what is not finite is computed again: of the columns that the block joined, and (by
+// the first block of a run) of the (group, head)s that the run wrote whole.
+template <typename T>
+__global__ __launch_bounds__(kThreads, 4) void k_attend_join(const AttendArgs a, const Split w) {
+    __shared__ Again s_again;
+    __shared__ unsigned s_beyond;
+    const Split::Join j = w.joins[blockIdx.x];
+    const int heads = a.kv_heads * w.parts;
+    const int64_t last = blockIdx.y == 0 ? j.beyond : -1;
+    int64_t next = last >= 0 ? j.whole : 0;
+    if (j.first < 0 && last < 0) return;
+    if (threadIdx.x == 0) s_beyond = 0;
+    bool joined = j.first >= 0;
+    if (joined) join_runs<T>(a, w, j, &s_beyond);
+    __syncthreads();
+    if (last < 0 && s_beyond == 0) return;           // as nearly always
+#pragma unroll 1
+    for (int64_t at = joined ? j.group * heads + j.head : next++; ; at = next++) {
+        const int64_t gi = at / heads;
+        const int head = static_cast<int>(at - gi * heads), kv = head / w.parts, part = head - kv * w.parts;
+        const Group grp = group_at(a, w, gi);
+        for (int k = threadIdx.x; !joined && k < columns_of(w, grp, part) * a.d; k += kThreads) {
+            const int c = k / a.d;
+            const Column col = column_of(w, grp, kv, part, c);
+            const T v = static_cast<const T*>(a.out)[col.seq * a.ldo + static_cast<int64_t>(col.head) * a.d + (k - c * a.d)];
+            if (!finite(static_cast<float>(v))) atomicOr(&s_beyond, 1u << c);
+        }
+        joined = false;
+        __syncthreads();
+        for (unsigned beyond = s_beyond; beyond; beyond &= beyond - 1) {
+            const Column col = column_of(w, grp, kv, part, __builtin_ctz(beyond));
+            attend_again<T>(a, s_again, col.seq, col.head);
+        }
+        if (next > last) return;
+        __syncthreads();
+        if (threadIdx.x == 0) s_beyond = 0;
+        __syncthreads();
     }
 }
 

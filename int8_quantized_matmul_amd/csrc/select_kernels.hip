@@ -40,14 +40,6 @@ __device__ __forceinline__ double lane_double(double v, int lane) {
 __device__ __forceinline__ float lane_value(float v, int lane) { return lane_float(v, lane); }
 __device__ __forceinline__ double lane_value(double v, int lane) { return lane_double(v, lane); }
 
-// -inf in fp64 from a register that the compiler does not look into: as a
-// constant of a whole wavefront it would become a scalar move of a 64-bit
-// literal, which this target has no encoding for and the compiler drops to 0.
-__device__ __forceinline__ double minus_infinity() {
-    float f = -INFINITY;
-    asm("" : "+v"(f));
-    return f;
-}
 template <typename V>
 __device__ __forceinline__ V least() {
     if constexpr (sizeof(V) == 8) return minus_infinity();
