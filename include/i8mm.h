@@ -813,7 +813,7 @@ size_t i8mm_decode_attention_workspace_bytes(int64_t n, int64_t heads, int64_t k
  * infinite value whose weight is rounded to 0 in 64 bits gives NaN. A head whose
  * fp32 result is not finite (bf16 values near fp32's end, infinities, NaN) is
  * computed again in 64 bits by one block, which takes longer: 0.1 ms for 2048
- * keys of 128 features, 5 ms for 100000.
+ * keys of 128 features, 6 ms for 100000.
  */
 i8mm_status i8mm_decode_attention(const void* Q, int64_t ldq, int32_t type, int64_t n, int64_t heads, int64_t kv_heads,
                                   int64_t d, const void* K_pages, int64_t k_stride, const void* V_pages,

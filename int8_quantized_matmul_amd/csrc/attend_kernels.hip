@@ -316,8 +316,10 @@ __global__ __launch_bounds__(kThreads) void k_attend_shared(const AttendArgs a, 
 // can give, from the definition: the keys' scores for the maximum, then once more for the
 // weights, a key a thread, and the values with 8 features a thread, of 256 / (d / 8) threads
 // that take the keys in turn. It is meant to be rare: one column of 2048 keys of 128 features
-// takes 90 us, of 100000 5.3 ms, all of 64 x 32 with 2048 1.1 ms on top of 0.4. (Smaller
-// weights instead would lose the smallest values, so they would have to follow the values.)
+// takes 110 us, of 100000 6.4 ms, all of 64 x 32 with 2048 1.4 ms on top of 0.4 (where the
+// scores hold a NaN or infinity, which ends it after the maximum, 40 us, 2.4 and 0.6 ms).
+// Smaller weights instead would lose the smallest values, so they would have to follow the
+// values.
 
 constexpr int kAgainAhead = 4;                   // loads of a thread on their way
 
@@ -348,9 +350,11 @@ __device__ __forceinline__ void attend_again(const AttendArgs& a, Again& s, int6
     typedef typename Vec8<T>::type vec;
     const int tid = static_cast<int>(threadIdx.x), len = clamped_len(a, seq), kv = head / (a.heads / a.kv_heads);
     const T* q = static_cast<const T*>(a.Q) + seq * a.ldq + static_cast<int64_t>(head) * a.d;
+    T* out = static_cast<T*>(a.out) + seq * a.ldo + static_cast<int64_t>(head) * a.d;
     const auto wide = [](T v) { return static_cast<double>(static_cast<float>(v)); };
     const int eights = a.d / 8, sharers = kThreads / eights, by = tid / eights, i = 8 * (tid - by * eights);
     double most = minus_infinity(), l = 0.0, o[8] = {};
+    const auto larger = [](double x, double y) { return y > x || y != y ? y : x; };   // (a NaN, if one of them is)
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -382,7 +386,7 @@ __device__ __forceinline__ void attend_again(const AttendArgs& a, Again& s, int6
                 if (a.slopes) x = __builtin_fma(static_cast<double>(a.slopes[head]), static_cast<double>(t - (len - 1)), x);
             }
             if (pass == 0) {
-                most = fmax(most, x);
+                most = larger(most, x);
                 continue;
             }
             const double w = there ? exp(x - most) : 0.0;
@@ -410,10 +414,18 @@ __device__ __forceinline__ void attend_again(const AttendArgs& a, Again& s, int6
                 }
             }
         }
-        if (pass == 0) most = over_block(s, most, [](double x, double y) { return fmax(x, y); });
+        if (pass > 0) break;
+        most = over_block(s, most, larger);
+        if (most - most == 0.0) continue;
+        // no number: it is the logarithm of the sum as well, and a weight is exp(inf - inf)
+        if (by == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[i + e] = static_cast<T>(NAN);
+        }
+        if (tid == 0 && a.lse) a.lse[seq * a.heads + head] = static_cast<float>(most);
+        return;
     }
     l = over_block(s, l, [](double x, double y) { return x + y; });
-    T* out = static_cast<T*>(a.out) + seq * a.ldo + static_cast<int64_t>(head) * a.d + i;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         s.value[tid] = o[e];
@@ -421,7 +433,7 @@ __device__ __forceinline__ void attend_again(const AttendArgs& a, Again& s, int6
         if (by == 0) {
             double sum = 0.0;
             for (int k = 0; k < sharers; ++k) sum += s.value[k * eights + tid];
-            out[e] = static_cast<T>(static_cast<float>(sum / l));
+            out[i + e] = static_cast<T>(static_cast<float>(sum / l));
         }
         __syncthreads();
     }

@@ -47,7 +47,7 @@ def attention(Q, K_pages, V_pages, tables, lens, scale, slopes=None) -> Tuple[np
             m = s.max()
             with np.errstate(invalid="ignore"):
                 w = np.exp(s - m)
-                lse[i, a] = m + np.log(w.sum())
+                lse[i, a] = m if np.isinf(m) else m + np.log(w.sum())
                 out[i, a] = (w / w.sum()) @ v[:, a // (heads // kv)]
     return out.reshape(n, heads * d), lse
 

@@ -89,3 +89,42 @@ def test_the_small_end_of_bf16():
     for std in (1e-35, 1e-37):
         V = pool(rng, tables, lens, pages, 2, page, d, BF16, std=std)
         _check(randn(rng, (2, 2 * d), BF16), K, V, tables, lens)
+
+
+def _exactly(q, K, V, tables, lens, beams=1, **kw):
+    """Heads that are all beyond fp32: computed in 64 bits, rounded to fp32 and to the output's type; what is no number
+    is the definition's."""
+    ro, rl = decode.attention(wide(q), wide(K), wide(V), tables, lens, float(np.float32(kw.get("scale", K.shape[3] ** -0.5))),
+                              None if kw.get("slopes") is None else wide(kw["slopes"]))
+    for t in (tables, _wider(tables, K.shape[2])):
+        out, lse = i8.decode_attention(q, K, V, ints(t), ints(lens), beams=beams, **kw)
+        torch.cuda.synchronize()
+        o, s = wide(out), wide(lse)
+        some = np.isfinite(ro)
+        assert np.array_equal(o[~some], ro[~some], equal_nan=True)
+        near(out[torch.as_tensor(some, device=DEV)], ro[some], 2.0 ** -23 * np.abs(ro[some]), "out")
+        with np.errstate(over="ignore"):
+            want = rl.astype(np.float32)
+        some = np.isfinite(want)
+        assert np.array_equal(s[~some], want[~some], equal_nan=True), (s[~some], want[~some])
+        assert (np.abs(s[some] - rl[some]) <= 2.0 ** -23 * np.abs(rl[some])).all()
+    return ro, rl
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_an_infinite_score(dtype):
+    """One key's score is infinite: so is the logarithm of the sum, and the result is no number (nor are both beside a NaN)."""
+    rng = np.random.default_rng(11)
+    lens, page, d = [50, 300, 1, 700], 16, 64
+    tables, pages = paged(rng, lens, page)
+    K, V = (pool(rng, tables, lens, pages, 2, page, d, dtype) for _ in range(2))
+    for i, n in enumerate(lens):
+        K[int(tables[i, (n - 1) // page]), :, (n - 1) % page, 5] = float("inf")
+    q = randn(rng, (4, 4 * d), dtype).abs()
+    say(f"  launch: decode_attention, an infinite score, {dtype}")
+    _, lse = _exactly(q, K, V, tables, lens)
+    assert np.isposinf(lse).all()
+    _exactly(q, K, V, tables, lens, beams=2)
+    K[int(tables[1, 0]), 1, 3, 0] = float("nan")
+    _, lse = _exactly(q, K, V, tables, lens)
+    assert np.isnan(lse[1, 2:]).all() and np.isposinf(lse[1, :2]).all()
