@@ -810,10 +810,10 @@ size_t i8mm_decode_attention_workspace_bytes(int64_t n, int64_t heads, int64_t k
  * I8MM_ATTENTION_WHOLE_KEYS (half of that if beams is more than 1).
  * What lies behind a sequence's last token never reaches it, NaN and infinity
  * included. Among its tokens they give what the formulas give, except that an
- * infinite value whose weight is rounded to 0 in 64 bits gives NaN. A head whose
- * fp32 result is not finite (bf16 values near fp32's end, infinities, NaN) is
- * computed again in 64 bits by one block, which takes longer: 0.1 ms for 2048
- * keys of 128 features, 6 ms for 100000.
+ * infinite value whose weight is rounded to 0 in 64 bits gives NaN. A head that
+ * leaves fp32's range in a score or in its result (bf16 queries, keys or values
+ * near fp32's end, infinities, NaN) is computed again in 64 bits by one block,
+ * which takes longer: 0.1 ms for 2048 keys of 128 features, 6 ms for 100000.
  */
 i8mm_status i8mm_decode_attention(const void* Q, int64_t ldq, int32_t type, int64_t n, int64_t heads, int64_t kv_heads,
                                   int64_t d, const void* K_pages, int64_t k_stride, const void* V_pages,

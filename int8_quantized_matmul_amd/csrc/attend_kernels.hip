@@ -153,6 +153,7 @@ __device__ __forceinline__ void add_step(Sums<EL>& sum, Step<NC, EL>& s, const Q
     typedef typename Vec8<T>::type vec;
     const int g = lane >> 4;
     float p[2][4];
+    float least = INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -162,19 +163,29 @@ __device__ __forceinline__ void add_step(Sums<EL>& sum, Step<NC, EL>& s, const Q
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             p[h][r] = __builtin_fmaf(q.bias, static_cast<float>(key + r - q.last), acc[r] * q.scale);
-            if (Alone) p[h][r] = mine ? p[h][r] : -INFINITY;
         }
+        float least_here = fminf(fminf(p[h][0], p[h][1]), fminf(p[h][2], p[h][3]));
         if (s.id[h] < 0 || s.key + h * kHalf + kHalf - 1 > last) {
             // keys that are not there: no weight, and whatever their slots hold stays out of the sums
+            least_here = INFINITY;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool there = s.id[h] >= 0 && key + r <= last;
+                least_here = there ? fminf(least_here, p[h][r]) : least_here;
                 p[h][r] = there ? p[h][r] : -INFINITY;
 #pragma unroll
                 for (int i = 0; i < EL / 2; ++i) s.v[h][r][i] = there ? s.v[h][r][i] : 0u;
             }
         }
+        least = fminf(least, least_here);
+        if (Alone) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[h][r] = mine ? p[h][r] : -INFINITY;
+        }
     }
+    // A score of -inf is one that fp32 has no room for (or a sum that has left it on the way),
+    // unless it is that of a key that is not there: its column is computed again.
+    if (least == -INFINITY && (!Alone || mine)) sum.l = NAN;
     float most = fmaxf(fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3])),
                        fmaxf(fmaxf(p[1][0], p[1][1]), fmaxf(p[1][2], p[1][3])));
     most = fmaxf(column_max(most), sum.m);
@@ -310,10 +321,11 @@ __global__ __launch_bounds__(kThreads) void k_attend_shared(const AttendArgs a, 
 
 // ---------------------------------------------------------------- beyond fp32
 //
-// A sum of values near fp32's end, or a weighted mean that its weights' rounding takes past
-// the type's largest number, is infinite, while the result is not. A column whose result is
-// not finite is computed again by a block in fp64, which has room for all that finite inputs
-// can give, from the definition: the keys' scores for the maximum, then once more for the
+// A sum of values near fp32's end, a weighted mean that its weights' rounding takes past the
+// type's largest number, or a score (or a part of its sum) beyond fp32 is infinite, while the
+// result is not. A column whose result is not finite, or of which a key has a score of -inf
+// (add_step() makes its sum a NaN then), is computed again by a block in fp64, which has room
+// for all that finite inputs can give, from the definition: the keys' scores for the maximum, then once more for the
 // weights, a key a thread, and the values with 8 features a thread, of 256 / (d / 8) threads
 // that take the keys in turn. It is meant to be rare: one column of 2048 keys of 128 features
 // takes 110 us, of 100000 6.4 ms, all of 64 x 32 with 2048 1.4 ms on top of 0.4 (where the

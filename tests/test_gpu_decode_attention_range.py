@@ -128,3 +128,90 @@ def test_an_infinite_score(dtype):
     K[int(tables[1, 0]), 1, 3, 0] = float("nan")
     _, lse = _exactly(q, K, V, tables, lens)
     assert np.isnan(lse[1, 2:]).all() and np.isposinf(lse[1, :2]).all()
+
+
+@pytest.mark.parametrize("beams", [1, 2])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scores_of_minus_infinity(dtype, beams):
+    """A key of score -inf has no weight beside others; where all are, the log-sum is -inf and the result no number. A
+    sequence without tokens still gives 0."""
+    rng = np.random.default_rng(12)
+    lens, page, d, heads = [1, 40, 300, 700, 0, 33], 16, 64, 2
+    tables, pages = paged(rng, lens, page)
+    K, V = (pool(rng, tables, lens, pages, heads, page, d, dtype) for _ in range(2))
+    q = randn(rng, (6, 2 * heads * d), dtype).abs()
+    for i in (0, 2):
+        K[ints(tables[i][tables[i] >= 0]).long(), :, :, 7] = float("-inf")
+    say(f"  launch: decode_attention, scores of -inf, {dtype}, beams {beams}")
+    ro, rl = _exactly(q[[0, 2]], K, V, tables[[0, 2]], [1, 300], beams=beams)
+    assert np.isneginf(rl).all() and np.isnan(ro).all()
+    for i, n in ((1, 40), (3, 700)):                  # all tokens but two
+        at = rng.choice(n, size=n - 2, replace=False)
+        K[ints(tables[i, at // page]).long(), :, ints(at % page).long(), 7] = float("-inf")
+    _exactly(q[[1, 3]], K, V, tables[[1, 3]], [40, 700], beams=beams)
+    out, lse = i8.decode_attention(q, K, V, ints(tables), ints(lens), beams=beams)
+    assert not out[4].any() and torch.isneginf(lse[4]).all() and torch.isfinite(out[5]).all()
+
+
+@pytest.mark.parametrize("beams", [1, 2])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_finite_scores_that_fp32_has_no_room_for(sign, beams):
+    """bf16's queries and keys are finite and their products are not in fp32, above and below; the largest score takes the
+    weight, equal ones share it, and the log-sum is what fp32 makes of it."""
+    rng = np.random.default_rng(13)
+    lens, page, d, heads = [1, 40, 700, 5], 16, 64, 2
+    tables, pages = paged(rng, lens, page)
+    K, V = pool(rng, tables, lens, pages, heads, page, d, BF16, std=0.0), pool(rng, tables, lens, pages, heads, page, d, BF16)
+    q = torch.full((4, 2 * heads * d), 1e20, dtype=BF16, device=DEV)
+    say(f"  launch: decode_attention, scores beyond fp32, sign {sign}, beams {beams}")
+    for i, n in enumerate(lens):                      # equal scores
+        K[ints(tables[i][tables[i] >= 0]).long()] += sign * 1e20
+    ro, rl = _exactly(q, K, V, tables, lens, beams=beams)
+    assert np.isfinite(ro).all() and (np.abs(rl) > 1e39).all()
+    # scores far apart: that of one key is the largest
+    for i, n in enumerate(lens):
+        for j in range(n):
+            K[int(tables[i, j // page]), :, j % page] *= 1.0 + (j != n // 2) * (1 if sign < 0 else -1) * (0.25 + 0.5 * rng.random())
+    ro, _ = _exactly(q, K, V, tables, lens, beams=beams)
+    for i, n in enumerate(lens):
+        v = wide(V[int(tables[i, n // 2 // page]), :, n // 2 % page]).reshape(-1)
+        assert np.array_equal(ro[i].reshape(heads, 2, d)[:, 0].reshape(-1), v)
+
+
+def test_sums_that_leave_fp32_on_the_way():
+    """Products of +-2e38 whose sum is a number of fp32, in orders of which any partial sum may be beyond it."""
+    page, d = 16, 16
+    q = torch.ones((1, d), dtype=BF16, device=DEV)
+    big = float(torch.tensor(2e38, dtype=BF16))
+    say("  launch: decode_attention, partial sums beyond fp32")
+    for order in range(6):
+        rng = np.random.default_rng(order)
+        K = torch.zeros((1, 1, page, d), dtype=BF16, device=DEV)
+        V = randn(rng, (1, 1, page, d), BF16)
+        # the sums: 3, -2e38 (which is the largest in the second call), 5
+        for j, row in enumerate(([big, big, -big, -big, 3.0], [-big, -big, big], [big, -big, 5.0])):
+            place = rng.permutation(d)[:len(row)]
+            K[0, 0, j, torch.as_tensor(place, device=DEV)] = torch.tensor(row, dtype=BF16, device=DEV)
+        out, lse = i8.decode_attention(q, K, V, ints([[0]]), ints([3]), scale=1.0)
+        # A sum of terms of 2e38 is off by up to (d + 4) 2^-24 * 8e38 = 1e33 in fp32, and by 1e24 in 64 bits, so which of 3
+        # and 5 is the larger is not determined, nor are the weights but for their being weights: the result lies between
+        # the values (beside the roundings of weights and result), and the log-sum within 1e33 of the definition's
+        v = wide(V)[0, 0, :3]
+        slack = 2.0 ** -7 * np.abs(v).max(0)
+        assert (wide(out)[0] >= v.min(0) - slack).all() and (wide(out)[0] <= v.max(0) + slack).all()
+        assert abs(float(lse)) <= 1e33
+        K[0, 0, 0] = -big                             # -3.2e39, -2e38
+        out, lse = i8.decode_attention(q, K, V, ints([[0]]), ints([2]), scale=1.0)
+        assert np.array_equal(wide(out)[0], wide(V)[0, 0, 1]) and abs(float(lse) + big) <= 2.0 ** -23 * big
+
+
+def test_a_scale_or_bias_beyond_fp32():
+    rng = np.random.default_rng(14)
+    lens, page, d = [1, 3, 300], 16, 64
+    tables, pages = paged(rng, lens, page)
+    K, V = (pool(rng, tables, lens, pages, 2, page, d, F16) for _ in range(2))
+    q = randn(rng, (3, 2 * d), F16, 30.0)
+    say("  launch: decode_attention, scales and biases beyond fp32")
+    for scale in (3e38, -3e38):
+        _exactly(q, K, V, tables, lens, scale=scale)
+    _exactly(q, K, V, tables, lens, slopes=torch.tensor([3e38, -3e38], device=DEV))
