@@ -1107,6 +1107,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     if given, comes back as [n k, T + 1], each row its parent's and the new
     token. A workspace, if given, is a uint8 tensor of beam_select_workspace(n,
     beams, vocab, k) bytes or more."""
+    if history is None and history_out is not None:
+        raise ValueError("history_out is written from history, which is missing")
     dev = _gpu_of(logits, "logits", _DTYPES)
     n, beams = scores.shape
     vocab = logits.shape[1]
