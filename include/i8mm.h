@@ -694,7 +694,8 @@ i8mm_status i8mm_clip_grad_norm(const void* const* grads, void* const* outs, con
  * * page < 2^31 - 4096), sequences of a call, features of a head (a multiple of
  * 8), rows of an append, beams of a request and continuations kept of one, tokens
  * of the vocabulary; and the positions of a sequence up to which the attention
- * takes no workspace. */
+ * takes no workspace. Strides are up to 2^40, and up to 2^60 over all rows or
+ * pages of an operand. */
 #define I8MM_CACHE_MAX_PAGES 16777216
 #define I8MM_CACHE_MAX_PAGE 4096
 #define I8MM_CACHE_MAX_ROW 1048576
