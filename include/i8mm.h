@@ -841,8 +841,9 @@ size_t i8mm_beam_select_workspace_bytes(int64_t n, int64_t beams, int64_t vocab,
  * history: [n beams, T] int32, row stride ldh, the beams' tokens so far, and
  * history_out: [n k, T + 1] (written, not history): the parents' rows and the
  * new tokens; NULL history_out for none (history, ldh, T and ldho are then not
- * looked at). Sums are fp32 over parts of a row and fp64 over the parts; t is
- * compared in fp64. workspace: i8mm_beam_select_workspace_bytes(...) bytes,
+ * looked at). Within a beam the order is that of the logits. Sums are fp32 over
+ * parts of a row and fp64 over the parts, which leaves log sum exp off by some
+ * 1e-7, 1e-5 at most; t is compared in fp64. workspace: i8mm_beam_select_workspace_bytes(...) bytes,
  * 256-byte aligned, contents unspecified before and after.
  */
 i8mm_status i8mm_beam_select(const void* logits, int64_t ld, int32_t type, int64_t n, int64_t beams, int64_t vocab,
