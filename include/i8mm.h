@@ -843,8 +843,9 @@ size_t i8mm_beam_select_workspace_bytes(int64_t n, int64_t beams, int64_t vocab,
  * new tokens; NULL history_out for none (history, ldh, T and ldho are then not
  * looked at). Within a beam the order is that of the logits. Sums are fp32 over
  * parts of a row and fp64 over the parts, which leaves log sum exp off by some
- * 1e-7, 1e-5 at most; t is compared in fp64. workspace: i8mm_beam_select_workspace_bytes(...) bytes,
- * 256-byte aligned, contents unspecified before and after.
+ * 1e-7, and by 6e-6 + 2e-10 vocab at most; t is compared in fp64. workspace:
+ * i8mm_beam_select_workspace_bytes(...) bytes, 256-byte aligned, contents
+ * unspecified before and after.
  */
 i8mm_status i8mm_beam_select(const void* logits, int64_t ld, int32_t type, int64_t n, int64_t beams, int64_t vocab,
                              const float* scores, int64_t k, float* scores_out, int32_t* parents, int32_t* tokens,

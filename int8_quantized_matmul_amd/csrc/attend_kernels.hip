@@ -23,12 +23,12 @@
 // good as the other sums, for 0.3 % of the time. (An infinite value times a second part that
 // is 0 or negative is no number; such a column is computed again, see attend_again().)
 //
-// 64 sequences x 96 heads of 128 features, up to 2048 tokens each (3.2 GB): 517 us,
-// 6.2 TB/s, and 8 us for joining. What it took: values loaded past the caches (568
-// with ordinary loads: a CU's L1 cache is smaller than what is in flight through
+// 64 sequences x 96 heads of 128 features, up to 2048 tokens each (3.2 GB): 528 us,
+// 6.1 TB/s, and 10 us for joining. What it took: values loaded past the caches (51 us
+// less than ordinary loads: a CU's L1 cache is smaller than what is in flight through
 // it), and runs of about 24 tiles in the order of the rows, so that the heads of
-// a page are read at about the same time (596 with one run a block, a twelfth of
-// the heads apart). A step's loads before the last one's products, or three blocks
+// a page are read at about the same time (79 us less than one run a block, a twelfth
+// of the heads apart). A step's loads before the last one's products, or three blocks
 // a CU, change nothing: the wavefronts of a CU cover for one another.
 
 #include "../../include/i8mm.h"
@@ -713,9 +713,9 @@ __global__ __launch_bounds__(kThreads, kBlocks<EL> / 256) void k_attend(const At
 // first ones, kJoinCols columns a block. Every 16 bytes of the result are summed by one
 // thread, or, where there are fewer of them than threads, by several that take the runs
 // in turn, kJoinAhead of each on their way at once; the runs' weights lie in shared
-// memory. One sequence of 12274 tokens, 64 heads on 4: 14.5 us, and 26 with a load after
+// memory. One sequence of 12274 tokens, 64 heads on 4: 13.5 us, and 26 with a load after
 // the other and the weights taken where they are used; 64 x 96 heads of two parts at most
-// 9 instead of 8. 16 on their way take 13 in each.
+// 10, and 1 less so. 16 on their way take 13 in each.
 constexpr int kJoinCols = 4;
 constexpr int kJoinAhead = 8;
 constexpr int kJoinRuns = 512;
@@ -904,11 +904,11 @@ hipError_t attend_type(const AttendArgs& a, void* workspace, hipStream_t stream)
 
 }  // namespace
 
-// Up to so many keys a block takes whole (group, head)s. At 1024: 12 heads of 128
-// sequences 123 us so and 132 split and joined, 32 heads of 16 41 and 47, of one 14 and 11
-// (but a launch less for the host); at 2048 96 heads of 64 993 and 982, and with lengths
-// that differ 532 and 515. Beams that share pages gain by the split path's groups, so
-// they take it earlier.
+// Up to so many keys a block takes whole (group, head)s. At 1000 keys: 12 heads of 128
+// sequences 123 us so and 130 split and joined, 32 heads of 16 43 and 48; 32, 12 or one
+// head of one sequence 14 and 12 on the GPU, but a call 14 and 15 to 16, as it launches one
+// kernel less. At 2048 96 heads of 64 993 and 982, and with lengths that differ 532 and 515.
+// Beams that share pages gain by the split path's groups, so they take it earlier.
 bool attention_takes_whole(int64_t keys, int64_t beams) { return keys * (beams > 1 ? 2 : 1) <= I8MM_ATTENTION_WHOLE_KEYS; }
 
 size_t decode_attention_scratch(int64_t n, int, int, int d) {
