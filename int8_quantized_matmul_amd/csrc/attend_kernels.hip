@@ -327,13 +327,13 @@ __global__ __launch_bounds__(kThreads) void k_attend_shared(const AttendArgs a, 
 // type's largest number, or a score (or a part of its sum) beyond fp32 is infinite, while the
 // result is not. A column whose result is not finite, or of which a key has a score of -inf
 // (add_step() makes its sum a NaN then), is computed again by a block in fp64, which has room
-// for all that finite inputs can give, from the definition: the keys' scores for the maximum, then once more for the
-// weights, a key a thread, and the values with 8 features a thread, of 256 / (d / 8) threads
-// that take the keys in turn. It is meant to be rare: one column of 2048 keys of 128 features
-// takes 110 us, of 100000 6.4 ms, all of 64 x 32 with 2048 1.4 ms on top of 0.4 (where the
-// scores hold a NaN or infinity, which ends it after the maximum, 40 us, 2.4 and 0.6 ms).
-// Smaller weights instead would lose the smallest values, so they would have to follow the
-// values.
+// for all that finite inputs can give, from the definition: the keys' scores for the maximum,
+// then once more for the weights, a key a thread, and the values with 8 features a thread, of
+// 256 / (d / 8) groups that take the keys in turn. It is meant to be rare: one column of 2048
+// keys of 128 features takes 110 us, of 100000 6.4 ms, all of 64 x 32 with 2048 1.4 ms on top
+// of 0.4 (where the scores hold a NaN or infinity, which ends it after the maximum, 40 us,
+// 2.4 and 0.6 ms). Smaller weights instead would lose the smallest values, so they would have
+// to follow the values.
 
 constexpr int kAgainAhead = 4;                   // loads of a thread on their way
 
@@ -464,7 +464,7 @@ struct Attend {
     float m[kWaves][kCols], l[kWaves][kCols];
     int64_t scan[kWaves];
     int64_t at_group, at_units;
-    unsigned beyond;         // the columns whose sums are not finite
+    unsigned beyond;         // the columns whose result is not finite
 };
 
 // Joins the wavefronts' sums; f(column, feature, o, m, l) for each, o and l relative to the maximum m.

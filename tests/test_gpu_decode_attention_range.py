@@ -215,3 +215,41 @@ def test_a_scale_or_bias_beyond_fp32():
     for scale in (3e38, -3e38):
         _exactly(q, K, V, tables, lens, scale=scale)
     _exactly(q, K, V, tables, lens, slopes=torch.tensor([3e38, -3e38], device=DEV))
+
+
+@pytest.mark.parametrize("beams", [1, 3])
+def test_captured_and_replayed_beyond_fp32_and_back(beams):
+    """One graph, replayed over values that leave fp32's range in some heads, in none, in scores, and on another stream:
+    the eager call's result each time, and the same one twice."""
+    rng = np.random.default_rng(15)
+    lens, page, d, heads = [200, 7, 700, 33, 0, 128], 16, 64, 4
+    tables, pages = paged(rng, lens, page)
+    tables = _wider(tables, page)
+    K, V = (torch.zeros((pages, 2, page, d), dtype=BF16, device=DEV) for _ in range(2))
+    q, t, n = torch.zeros((6, heads * d), dtype=BF16, device=DEV), ints(tables), ints(lens)
+    out, lse = torch.empty_like(q), torch.empty((6, heads), device=DEV)
+    ws = torch.empty(i8.decode_attention_workspace(6, heads, 2, d), dtype=torch.uint8, device=DEV)
+    say(f"  launch: decode_attention beyond fp32, captured, beams {beams}")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        i8.decode_attention(q, K, V, t, n, out=out, lse=lse, beams=beams, workspace=ws)
+    side = torch.cuda.Stream()
+    for step in range(6):
+        k, v = (pool(rng, tables, lens, pages, 2, page, d, BF16) for _ in range(2))
+        if step % 3 == 0:
+            v[::3, 1] = 3e38
+        if step % 3 == 1:
+            k[::2, 0] *= 1e30
+        x = randn(rng, (6, heads * d), BF16, 1e12 if step == 4 else 1.0)
+        for a, b in ((K, k), (V, v), (q, x)):
+            a.copy_(b)
+        ws.random_(0, 255)
+        g.replay()
+        eager = i8.decode_attention(q, K, V, t, n, beams=beams)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = i8.decode_attention(q, K, V, t, n, beams=beams)
+        torch.cuda.synchronize()
+        assert torch.isfinite(out).all()
+        for a, b in (eager, other):
+            assert torch.equal(out, a) and torch.equal(lse, b)
